@@ -457,6 +457,177 @@ tq_status tq_prefill_attn(const tq_quantizer* kq, const tq_quantizer* vq, const 
                           tq_packed vcache, float scale, float* out, void* workspace, size_t ws_bytes,
                           tq_stream stream);
 
+/*
+ * 8-bit block-scaled cache: keys and values as e4m3 codes with one fp32 scale, a power of two,
+ * for each block of TQ_KV8_BLOCK consecutive tokens of a head; x^ = code * scale.  Beside the
+ * packed TurboQuant records it is the form for models whose cache keeps 8 bits a value: no
+ * rotation, no codebook, and every option of the scores below.
+ * A side of the cache holds codes [records][d] (d = 64 or 128 bytes a record) and scales
+ * [records / TQ_KV8_BLOCK].  Records are laid out [B][Hkv][Nmax] (Nmax a multiple of
+ * TQ_KV8_BLOCK), or as a paged pool (tq_pages above).  A side has fewer than 2^31 records.
+ */
+#define TQ_KV8_BLOCK 16
+
+typedef struct {
+  uint8_t* codes;
+  float* scales;
+} tq_kv8;
+
+/* Element strides of rows [B][H][T][d] whose d elements are contiguous; rows must stay 16-byte
+ * aligned.  Where a tq_strides* is NULL the array is contiguous. */
+typedef struct {
+  int64_t b, h, t;
+} tq_strides;
+
+/*
+ * How attention over the 8-bit cache scores.  A query of head hq at position pos gives token t
+ *   s = scale * <q, k^_t>;  with softcap > 0, s = softcap * tanh(s / softcap);
+ *   with slopes, s -= slopes[hq] * |pos - t|;
+ * and it sees token t iff
+ *   t < kv_lens[b],  t <= pos or t < prefix[b],  t >= first[b * T + i],  t > pos - window
+ * (each of the last three only where given; window 0 = none).  So first holds the start of the
+ * query's document in a packed sequence, prefix the tokens that all queries see.  A query that
+ * sees nothing, and one with pos < 0 (padding), gets out = 0 and lse = -inf.  All pointers are
+ * DEVICE: slopes [Hq] fp32, first [B][T] and prefix [B] int32, each may be NULL.  A tq_scoring*
+ * of NULL means scale = 1 / sqrt(d) and no option.
+ */
+typedef struct {
+  float scale;
+  float softcap;          /* 0 = none */
+  const float* slopes;
+  int32_t window;         /* 0 = none */
+  const int32_t* first;
+  const int32_t* prefix;
+} tq_scoring;
+
+/*
+ * DEVICE.  Writes new tokens behind those that the cache holds: k_new / v_new [B][Hkv][T][d]
+ * (dtype, strides or NULL).  kv_lens [B] (device int32) counts the tokens including the new
+ * ones, of which sequence b brings new_lens[b] (0..T; NULL: T each), rows 0..new_lens[b]-1 of
+ * its T: token kv_lens[b] - new_lens[b] + i is row i.  For each block of a head that gets new
+ * tokens, with amax their largest magnitude,
+ *   s = the smallest power of two >= 2^-126 with amax <= 448 s; where the block holds earlier
+ *   tokens, s = max(s, its scale) and their codes become e4m3(code * old scale / s);
+ *   code = e4m3(x / s), to nearest, ties to even.
+ * Records behind the last token keep their bytes.  A sequence whose lengths do not fit (new
+ * tokens more than T or than kv_lens, kv_lens over capacity) is left alone and sets the device
+ * status to TQ_ERR_INVALID_ARG.  Two sequences must not share a page that gets tokens.
+ */
+tq_status tq_kv8_append(const void* k_new, const void* v_new, int32_t dtype, const tq_strides* k_strides,
+                        const tq_strides* v_strides, int32_t B, int32_t Hkv, int32_t T, int32_t d,
+                        const int32_t* kv_lens, const int32_t* new_lens, const tq_pages* pages, int64_t Nmax,
+                        tq_kv8 kcache, tq_kv8 vcache, tq_stream stream);
+
+/* Workspace bytes of the attention calls below (T = 1 for decode; Nmax = max_pages * page_size
+ * for a paged cache). */
+tq_status tq_kv8_attn_workspace(int32_t dtype, int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t d, int64_t Nmax,
+                                size_t* bytes);
+
+/*
+ * DEVICE.  One decode step over the 8-bit cache: for every (b, query head), the query sits at
+ * position kv_lens[b] - 1 and, with KV head h / (Hq/Hkv),
+ *   out = sum_t softmax_t(s) v^_t,   lse = ln sum_t e^s   (scores as tq_scoring).
+ * q [B][Hq][d] (dtype; q_strides.t unused), out [B][Hq][d] of the same dtype, lse [B][Hq] fp32
+ * or NULL.  kv_lens[b] may be 0.  With k_new / v_new [B][Hkv][d] (both or neither; strides .b
+ * and .h) the step's token kv_lens[b] - 1 is appended first, as tq_kv8_append with T = 1.
+ * pages NULL: the [B][Hkv][Nmax] layout; else Nmax is ignored.  A length outside 0..capacity
+ * is read as the nearest bound and reported; NaN codes of value records that some query of the
+ * step does not see are read as 0, so they never reach it.
+ */
+tq_status tq_kv8_decode_attn(const void* q, const tq_strides* q_strides, int32_t dtype, int32_t B, int32_t Hq,
+                             int32_t Hkv, int32_t d, const int32_t* kv_lens, const tq_scoring* scoring,
+                             const tq_pages* pages, int64_t Nmax, const void* k_new, const void* v_new,
+                             const tq_strides* k_strides, const tq_strides* v_strides, tq_kv8 kcache, tq_kv8 vcache,
+                             void* out, float* lse, void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * DEVICE.  Attention of T queries per sequence over the 8-bit cache: query (b, h, i) sits at
+ * q_pos[b * T + i] (device int32 [B][T]; below 0 = padding).  q and out [B][Hq][T][d] (dtype),
+ * lse [B][Hq][T] fp32 or NULL.  The cache already holds the block's own tokens (tq_kv8_append
+ * first).  Otherwise as tq_kv8_decode_attn.
+ */
+tq_status tq_kv8_prefill_attn(const void* q, const tq_strides* q_strides, int32_t dtype, int32_t B, int32_t Hq,
+                              int32_t Hkv, int32_t T, int32_t d, const int32_t* q_pos, const int32_t* kv_lens,
+                              const tq_scoring* scoring, const tq_pages* pages, int64_t Nmax, tq_kv8 kcache,
+                              tq_kv8 vcache, void* out, float* lse, void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * Page pool of a cache of any kind (packed TurboQuant records or the 8-bit cache): which pages
+ * each row (sequence) holds, and how many rows hold each page.  block_table [rows][max_pages]
+ * and refs [num_pages] are DEVICE int32 owned by the caller; refs 0 = free, start them at 0.
+ * A row of len tokens holds its first ceil(len / page_size) entries; entries behind them are
+ * not read.  Free pages are taken lowest id first, in the order of the requests, so that a
+ * call's result depends on its arguments alone.
+ * A pool array is one array of the cache's records ([num_pages][page_bytes]: for the 8-bit
+ * cache page_bytes = Hkv * page_size * d of codes, Hkv * page_size / TQ_KV8_BLOCK * 4 of
+ * scales); page_bytes is a multiple of 4.
+ */
+#define TQ_MAX_POOL_ARRAYS 16
+
+typedef struct {
+  int32_t* block_table;
+  int32_t* refs;
+  int32_t rows;
+  int32_t max_pages;
+  int32_t page_size;
+  int64_t num_pages;
+} tq_page_pool;
+
+typedef struct {
+  void* data;
+  int64_t page_bytes;
+} tq_pool_array;
+
+/* Workspace bytes of reserve and fork with n requests, and of compact. */
+tq_status tq_pages_workspace(const tq_page_pool* pool, int32_t n, size_t* bytes);
+
+/*
+ * DEVICE.  Gives back the pages of rows[i] (its first ceil(lens[i] / page_size) entries), i < n:
+ * counts go down by one, the entries become -1.  An entry that is -1 already is skipped, so a
+ * row named twice gives its pages back once.  A row or length out of range, and a page that is
+ * free already, are skipped and set the device status to TQ_ERR_INVALID_ARG.
+ */
+tq_status tq_pages_free(const tq_page_pool* pool, const int32_t* rows, const int32_t* lens, int32_t n, tq_stream stream);
+
+/*
+ * DEVICE.  Grows rows[i] from old_lens[i] to new_lens[i] tokens: the entries between the two
+ * page counts get free pages (count 1).  Rows are distinct.  All or nothing: *shortfall (device
+ * int32) is 0 when done; else nothing changed and it holds the number of pages lacking, or -1
+ * for a repeated row or one out of range, or a length out of range (device status
+ * TQ_ERR_INVALID_ARG).
+ */
+tq_status tq_pages_reserve(const tq_page_pool* pool, const int32_t* rows, const int32_t* old_lens,
+                           const int32_t* new_lens, int32_t n, int32_t* shortfall, void* workspace, size_t ws_bytes,
+                           tq_stream stream);
+
+/*
+ * DEVICE.  Makes row dst[i] continue from the first lens[i] tokens of row src[i]: whole pages
+ * are shared (count + 1); a partly filled last page is copied, in every array, to a free page,
+ * so that both rows can append.  dst rows are distinct, hold no pages and are none of src; one
+ * src may be named many times.  All or nothing, with *shortfall as tq_pages_reserve.
+ */
+tq_status tq_pages_fork(const tq_page_pool* pool, const tq_pool_array* arrays, int32_t n_arrays, const int32_t* src,
+                        const int32_t* dst, const int32_t* lens, int32_t n, int32_t* shortfall, void* workspace,
+                        size_t ws_bytes, tq_stream stream);
+
+/*
+ * DEVICE.  Closes the pool up: with L pages in use (*live, device int32), those with ids >= L
+ * move, in their order, to the free ids below L, in every array, in refs and in all entries of
+ * the block table (entries < 0 stay, entries of free pages become -1).  page_map [num_pages]
+ * (device int32) receives each page's new id, -1 for a free one.  Moved-from pages keep their
+ * bytes.
+ */
+tq_status tq_pages_compact(const tq_page_pool* pool, const tq_pool_array* arrays, int32_t n_arrays, int32_t* page_map,
+                           int32_t* live, void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * DEVICE.  Copies page src[i] to page dst[i] in every array, i < n (device int32 lists).  The
+ * dst pages are distinct and none of src (other than dst[i] = src[i]); a pair with an id out of
+ * range is skipped and sets the device status to TQ_ERR_INVALID_ARG.
+ */
+tq_status tq_pages_copy(const tq_pool_array* arrays, int32_t n_arrays, int64_t num_pages, const int32_t* src,
+                        const int32_t* dst, int32_t n, tq_stream stream);
+
 /* Size of the fixed device scratch array behind tq_decode_attn_fixed_ws (8 MiB per device). */
 #define TQ_DECODE_FIXED_WS_BYTES (8u << 20)
 

@@ -1,0 +1,106 @@
+// Shared pieces of the 8-bit block-scaled cache (append, decode and prefill attention).
+//
+// A side of the cache (keys or values) is e4m3 codes [records][d] with one fp32 scale, a power
+// of two, for each block of 16 records of a head: x^ = code * scale.  Record of token t of
+// sequence b and head h: (page * Hkv + h) * page_size + t % page_size, page = block_table[b *
+// max_pages + t / page_size]; without a block table page = b and page_size = Nmax, which is the
+// contiguous layout [B][Hkv][Nmax].
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "device_common.cuh"
+
+namespace tq {
+
+constexpr int kKv8Block = TQ_KV8_BLOCK;
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Kv8Map {
+  const int32_t* table;   // [B][max_pages], or nullptr (contiguous)
+  int64_t page;           // page_size, or Nmax
+  int max_pages;
+  int64_t num_pages;      // pages of the pool, or B
+  int Hkv;
+  int64_t cap;            // tokens a sequence can hold
+};
+
+// Record of token t; an id outside the pool is read as page 0 and reported.
+__device__ __forceinline__ int64_t kv8_record(const Kv8Map& m, int b, int h, int64_t t, int* status) {
+  if (!m.table) return (static_cast<int64_t>(b) * m.Hkv + h) * m.page + t;
+  const int page = static_cast<int>(m.page);
+  const int ti = static_cast<int>(t), col = ti / page;
+  int64_t id = __ldg(m.table + static_cast<int64_t>(b) * m.max_pages + col);
+  if (id < 0 || id >= m.num_pages) {
+    report_status(status, TQ_ERR_INVALID_ARG);
+    id = 0;
+  }
+  return (id * m.Hkv + h) * page + (ti - col * page);
+}
+
+// Which tokens a query at `pos` sees, and how its scores are formed.
+struct Kv8Scoring {
+  const int32_t* kv_lens;   // [B]
+  const int32_t* q_pos;     // [B][T], or nullptr: the sequence's last token
+  const int32_t* first;     // [B][T] or nullptr
+  const int32_t* prefix;    // [B] or nullptr
+  const float* slopes;      // [Hq] or nullptr
+  int window;
+  float scale_log2;         // scale * log2(e): scores in powers of two
+  float cap;                // 0: none.  scores are cap * tanh(score / cap)
+};
+
+// Visible tokens [lo, hi) of query (b, i); hi <= lo: none.  len is already within capacity.
+__device__ __forceinline__ void kv8_range(const Kv8Scoring& s, int b, int i, int T, int len, int& lo, int& hi, int& pos) {
+  pos = s.q_pos ? __ldg(s.q_pos + static_cast<int64_t>(b) * T + i) : len - 1;
+  lo = 0;
+  hi = 0;
+  if (pos < 0) return;                       // padding
+  int64_t end = static_cast<int64_t>(pos) + 1;
+  if (s.prefix) end = max(end, static_cast<int64_t>(__ldg(s.prefix + b)));
+  hi = static_cast<int>(min(end, static_cast<int64_t>(len)));
+  if (s.window > 0) lo = max(lo, pos - s.window + 1);
+  if (s.first) lo = max(lo, __ldg(s.first + static_cast<int64_t>(b) * T + i));
+}
+
+// Length of sequence b; one outside 0..capacity is reported and read as the nearest bound.
+__device__ __forceinline__ int kv8_len(const int32_t* lens, int b, int64_t cap, int* status) {
+  const int n = __ldg(lens + b);
+  if (n < 0 || n > cap) {
+    report_status(status, TQ_ERR_INVALID_ARG);
+    return n < 0 ? 0 : static_cast<int>(cap);
+  }
+  return n;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh from 1 - 2 / (1 + e^2x): absolute error near 2^-22, which the cap scales.
+__device__ __forceinline__ float kv8_tanh(float x) {
+  return 1.f - __fdividef(2.f, 1.f + ex2(fminf(x * (2.f * kLog2E), 80.f)));
+}
+
+// Two e4m3 codes (low 16 bits) as two halves; every e4m3 value is exact in half precision.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+// The NaN codes (0x7f, 0xff) of four bytes as 0.
+__device__ __forceinline__ uint32_t e4m3_nan_to_zero(uint32_t w) {
+  const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+  return w & ~(nan * 0xffu);
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {   // a in the low half
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace tq

@@ -1,0 +1,670 @@
+// Attention of up to 16 query rows a key head over the 8-bit block-scaled cache: decode steps,
+// short query blocks, and fp32 queries of any length in groups of 16 rows.
+//
+//   l_t = scale q.k^_t (capped, biased),  out = sum_t softmax(l)_t v^_t,  lse = ln sum_t e^{l_t}
+//
+// Bytes bound it: each token of a key head is 2 d codes and 2 / 16 scales, read once for all its
+// query rows.  The launch has one CTA an SM; the tiles of 32 tokens of all (sequence, key head)
+// pairs form one line that is cut into equal runs, one a CTA, so ragged lengths and few long
+// sequences load every SM alike.  A pair that one run covers is finished in the CTA; the others
+// leave at most two partial results a CTA, joined by a second, small kernel.
+//
+// Inside a CTA eight warps work without meeting: each keeps its own ring of tiles, copied by the
+// tensor-map engine into swizzled rows (the swizzle frees the reads of the value operand from
+// bank conflicts) and takes every eighth tile.  A tile's scores are S^T = K Q^T with 16 tokens as
+// the rows of an m16n8k16 product and eight query rows as its columns, so small groups of query
+// heads waste little of it; then O^T += V^T P^T with the dims as rows.  Codes become halves
+// (exact) on the way into the registers.  The order of the 16 dims of a step is free, as long as
+// q has it too: a lane reads 16 consecutive bytes of a row.
+//
+// Number ranges.  q is divided by a power of two a row so that its largest entry is in [1, 2) as
+// a half (entries below 2^-14 of it round to 2^-25 of it).  A value block's scale 2^e joins its
+// probabilities: P = p 2^(15 + e - E) with E the largest e so far, in halves of 11 bits down to
+// p 2^(e - E) = 2^-29.  fp32 queries take q and P as two halves each (22 bits).  Scores, maxima,
+// sums and outputs are fp32.
+#include <cuda_runtime.h>
+
+#include "kv8_launch.h"
+#include "launchers.h"
+#include "quantize_umma.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 32;                  // tokens
+constexpr int kMinTiles = kWarps;          // a CTA's run, where there is little work
+
+__host__ __device__ constexpr int ring_stages(int D, int NT) { return D == 64 ? 4 : (NT == 1 ? 3 : 2); }
+__host__ __device__ constexpr uint32_t stage_bytes(int D) { return 2u * kTile * D; }
+
+struct DecodeSmem {
+  uint32_t scales, bars, lo, hi, pref, ml, o, total;
+};
+__host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT) {
+  const int ns = ring_stages(D, NT);
+  DecodeSmem L{};
+  uint32_t at = kWarps * ns * stage_bytes(D);
+  L.o = at; at += 4u * 8 * NT * D * 4;                         // four warps' outputs
+  L.scales = at; at += kWarps * ns * 16;
+  L.bars = at; at += kWarps * ns * 8;
+  L.ml = at; at += kWarps * (16 * 2 + 1) * 4;                  // m, l of 16 rows and E
+  L.lo = at; at += kKv8DecodeMaxVB * 4;
+  L.hi = at; at += kKv8DecodeMaxVB * 4;
+  L.pref = at; at += (kKv8DecodeMaxVB + 1) * 4;
+  L.total = at + 16 + 1024;                                    // abort flag, alignment
+  return L;
+}
+static_assert(decode_smem(128, 1).total <= 232448 && decode_smem(128, 2).total <= 232448, "shared memory");
+
+// plan[]: [0] tiles a CTA, [1] virtual sequences, [2 ..] tiles before each (per key head)
+constexpr int kPlanHead = 2;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ float h_lo(float x) { return x - __half2float(__float2half_rn(x)); }
+
+// Address of byte `off` (16-byte chunk aligned) of row r in a tile of rows of D bytes, as the
+// tensor-map engine swizzles them: 16-byte chunks XORed with the row within 8 rows of 128 bytes
+// (D = 128) or with the pair of rows within 8 of 64 bytes (D = 64).
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, uint32_t off) {
+  return D == 128 ? r * 128u + (off ^ ((r & 7u) << 4)) : r * 64u + (off ^ (((r >> 1) & 3u) << 4));
+}
+
+// The place of a warp in the line of tiles.
+struct Place {
+  int v, h, tile, n;      // virtual sequence, key head, tile and tiles of the sequence
+};
+
+__device__ __forceinline__ Place place_of(int64_t u, const int* pref, int VB, int Hkv) {
+  int lo = 0, hi = VB - 1;
+  while (lo < hi) {                       // last v with Hkv * pref[v] <= u
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(pref[mid]) * Hkv <= u) lo = mid; else hi = mid - 1;
+  }
+  Place p;
+  p.v = lo;
+  p.n = pref[lo + 1] - pref[lo];
+  const int rem = static_cast<int>(u - static_cast<int64_t>(pref[lo]) * Hkv);
+  p.h = p.n ? rem / p.n : 0;
+  p.tile = p.n ? rem - p.h * p.n : 0;
+  return p;
+}
+
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const Kv8AttnParams p) {
+  constexpr int NS = ring_stages(D, NT);
+  constexpr uint32_t SB = stage_bytes(D);
+  constexpr DecodeSmem L = decode_smem(D, NT);
+  constexpr int KJ = D / 64;               // 64-dim halves of a row
+  constexpr int MT = D / 16;               // 16-dim rows of the output product
+  extern __shared__ unsigned char dsm_raw[];
+  const uint32_t raw = smem_u32(dsm_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sm = dsm_raw + (base - raw);
+  int* s_lo = reinterpret_cast<int*>(sm + L.lo);         // visible tokens [lo, hi) of a virtual sequence
+  int* s_hi = reinterpret_cast<int*>(sm + L.hi);
+  int* s_pref = reinterpret_cast<int*>(sm + L.pref);
+  float* s_ml = reinterpret_cast<float*>(sm + L.ml);
+  float* s_o = reinterpret_cast<float*>(sm + L.o);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.total - 1024 - 16);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, qd = lane & 3;
+  const uint32_t ring = base + warp * NS * SB;
+  const uint32_t bar0 = base + L.bars + warp * NS * 8;
+  const uint32_t sc0 = base + L.scales + warp * NS * 16;
+  if (lane == 0)
+    for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 5);
+  if (tid == 0) {
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
+  // ---- how the work is cut
+  const int VB = p.VB, Hkv = p.map.Hkv, R = p.T * p.G;
+  for (int v = tid; v < VB; v += kWarps * 32) {
+    const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
+    const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, p.status);
+    int lo = INT32_MAX, hi = 0;
+    const int i1 = min(R - 1, r0 + kKv8DecodeRows - 1) / p.G;
+    for (int i = r0 / p.G; i <= i1; ++i) {
+      int a, z, pos;
+      kv8_range(p.sc, b, i, p.T, len, a, z, pos);
+      if (z > a) { lo = min(lo, a); hi = max(hi, z); }
+    }
+    s_lo[v] = hi > 0 ? lo : 0;
+    s_hi[v] = hi;
+    s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {                         // prefix sums, 32 at a time
+    int run = 0;
+    for (int v = 0; v < VB; v += 32) {
+      int x = v + lane < VB ? s_pref[v + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (v + lane < VB) s_pref[v + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_pref[0] = 0;
+  }
+  __syncthreads();
+  const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
+  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinTiles));
+  if (blockIdx.x == 0) {
+    for (int v = tid; v <= VB; v += kWarps * 32) p.plan[kPlanHead + v] = s_pref[v];
+    if (tid == 0) { p.plan[0] = static_cast<int>(per); p.plan[1] = VB; }
+  }
+  pdl_trigger();
+  const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
+
+  // ---- issue side: this warp's tiles u0 + warp, + kWarps, ...
+  int64_t iu = u0 + warp;
+  Place ip{};
+  if (iu < u1) ip = place_of(iu, s_pref, VB, Hkv);
+  int issued = 0, used = 0;
+  auto issue = [&]() {
+    if (iu >= u1) return;
+    const int st = issued % NS;
+    const uint32_t bar = bar0 + 8 * st, dst = ring + st * SB;
+    if (lane < 4) {
+      const int b = (p.v0 + ip.v) / p.RG;
+      // a block outside the visible tokens may have no page: the nearest visible one instead
+      const int lo = s_lo[ip.v], hi = s_hi[ip.v];
+      const int blk = min(max((lo / kTile + ip.tile) * 2 + (lane & 1), lo / kKv8Block), (hi - 1) / kKv8Block);
+      const int64_t rec = kv8_record(p.map, b, ip.h, static_cast<int64_t>(blk) * kKv8Block, p.status);
+      if (lane == 0) mbar_expect_tx(bar, SB);
+      __syncwarp(0xfu);
+      if (lane < 2) {
+        const uint32_t off = (lane & 1) * kKv8Block * D;
+        const int row = static_cast<int>(rec);
+        tma_load_2d(dst + off, &kmap, 0, row, bar);
+        tma_load_2d(dst + kTile * D + off, &vmap, 0, row, bar);
+      }
+      const float* src = ((lane & 2) ? p.vscales : p.kscales) + rec / kKv8Block;
+      const uint32_t to = sc0 + st * 16 + lane * 4;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    }
+    __syncwarp();
+    ++issued;
+    iu += kWarps;
+    ip.tile += kWarps;
+    while (ip.tile >= ip.n && iu < u1) {
+      ip.tile -= ip.n;
+      if (++ip.h == Hkv) {
+        ip.h = 0;
+        do { ++ip.v; ip.n = s_pref[ip.v + 1] - s_pref[ip.v]; } while (ip.n == 0);
+      }
+    }
+  };
+  for (int s = 0; s < NS; ++s) issue();
+
+  // ---- consume side, one (sequence, key head) at a time
+  int64_t cu = u0 + warp;
+  bool dead = false;
+  for (int64_t u = u0; u < u1;) {
+    const Place sp = place_of(u, s_pref, VB, Hkv);
+    const int64_t seg_end = min(u1, u + sp.n - sp.tile);
+    const int gv = p.v0 + sp.v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
+    const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, nullptr);
+
+    // the query rows as the columns of the score product: row nt * 8 + g
+    uint32_t qf[W][NT][KJ * 8];
+    float qs[NT];                              // of row nt * 8 + g, then of this lane's score columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + nt * 8 + g;
+      float x[KJ][16];
+      float mx = 0.f;
+      const bool on = r < R;
+      const int i = on ? r / p.G : 0, hq = sp.h * p.G + (on ? r - i * p.G : 0);
+      const int64_t at = b * p.q_stride_b + hq * p.q_stride_h + i * p.q_stride_t;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; k += 8) {
+          const int64_t e = at + 64 * j + 16 * qd + k;
+          if (!on) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) x[j][k + z] = 0.f;
+          } else if (W == 2) {
+            const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
+            const float4 a = __ldg(s), c = __ldg(s + 1);
+            x[j][k] = a.x; x[j][k + 1] = a.y; x[j][k + 2] = a.z; x[j][k + 3] = a.w;
+            x[j][k + 4] = c.x; x[j][k + 5] = c.y; x[j][k + 6] = c.z; x[j][k + 7] = c.w;
+          } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e));
+            const uint32_t w4[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              float2 f;
+              if (p.dtype == TQ_BF16) f = make_float2(__uint_as_float(w4[z] << 16), __uint_as_float(w4[z] & 0xffff0000u));
+              else f = __half22float2(*reinterpret_cast<const __half2*>(&w4[z]));
+              x[j][k + 2 * z] = f.x;
+              x[j][k + 2 * z + 1] = f.y;
+            }
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(x[j][k]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 1), 253);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      qs[nt] = __uint_as_float(static_cast<uint32_t>(e) << 23) * p.sc.scale_log2;
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const float a = x[j][k] * down, c = x[j][k + 1] * down;
+          qf[0][nt][j * 8 + k / 2] = pack_h2(a, c);
+          if constexpr (W == 2) qf[1][nt][j * 8 + k / 2] = pack_h2(h_lo(a), h_lo(c));
+        }
+    }
+    // this lane's score columns: rows nt * 8 + 2 qd + c
+    float cs[NT][2], slope[NT][2], m[NT][2], l[NT][2];
+    int lo[NT][2], hi[NT][2], pos[NT][2];
+    int in_lo = 0, in_hi = INT32_MAX;            // tokens that every row sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        cs[nt][c] = __shfl_sync(0xffffffffu, qs[nt], (2 * qd + c) * 4);
+        const int r = r0 + nt * 8 + 2 * qd + c;
+        lo[nt][c] = hi[nt][c] = pos[nt][c] = 0;
+        slope[nt][c] = 0.f;
+        if (r < R) {
+          const int i = r / p.G;
+          kv8_range(p.sc, b, i, p.T, len, lo[nt][c], hi[nt][c], pos[nt][c]);
+          if (p.sc.slopes) slope[nt][c] = __ldg(p.sc.slopes + sp.h * p.G + r - i * p.G) * kLog2E;
+          in_lo = max(in_lo, lo[nt][c]);
+          in_hi = min(in_hi, hi[nt][c]);
+        }
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+      }
+    in_lo = __reduce_max_sync(0xffffffffu, in_lo);
+    in_hi = __reduce_min_sync(0xffffffffu, in_hi);
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.f;
+    int E = 1;                                   // largest value-scale exponent so far (biased)
+
+    for (; cu < seg_end; cu += kWarps) {
+      const int st = used % NS;
+      const uint32_t bar = bar0 + 8 * st, ks_a = ring + st * SB, vs_a = ks_a + kTile * D;
+      if (!dead && !mbar_wait(bar, (used / NS) & 1, p.wait_limit, p.status, abort_flag)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) continue;
+      ++used;
+      const int t0 = (s_lo[sp.v] / kTile + sp.tile + static_cast<int>(cu - u)) * kTile;
+      const bool masked = t0 < in_lo || t0 + kTile > in_hi;
+      float4 sc;                                 // key scales, value scales of the two blocks
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(sc.x), "=f"(sc.y), "=f"(sc.z), "=f"(sc.w)
+                   : "r"(sc0 + st * 16));
+
+      // scores
+      float s[2][NT][4];
+#pragma unroll
+      for (int bl = 0; bl < 2; ++bl) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[bl][nt][k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+          const int row = bl * 16 + g;
+          const uint4 ka = lds128(ks_a + swz<D>(row, 64 * j + 16 * qd));
+          const uint4 kb = lds128(ks_a + swz<D>(row + 8, 64 * j + 16 * qd));
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = e4m3x2_to_h2(wa[k]), a1 = e4m3x2_to_h2(wb[k]);
+            const uint32_t a2 = e4m3x2_to_h2(wa[k] >> 16), a3 = e4m3x2_to_h2(wb[k] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(s[bl][nt], a0, a1, a2, a3, qf[0][nt][j * 8 + 2 * k], qf[0][nt][j * 8 + 2 * k + 1]);
+              if constexpr (W == 2)
+                mma_f16(s[bl][nt], a0, a1, a2, a3, qf[1][nt][j * 8 + 2 * k], qf[1][nt][j * 8 + 2 * k + 1]);
+            }
+          }
+        }
+      }
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+      for (int bl = 0; bl < 2; ++bl) {
+        const float kscale = bl ? sc.y : sc.x;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = k & 1, t = t0 + bl * 16 + g + (k >> 1) * 8;
+            float x = s[bl][nt][k] * (kscale * cs[nt][c]);
+            if (p.sc.cap > 0.f) x = p.sc.cap * kLog2E * kv8_tanh(x * (kLn2 / p.sc.cap));
+            if (p.sc.slopes) x -= slope[nt][c] * static_cast<float>(abs(pos[nt][c] - t));
+            if (masked && (t < lo[nt][c] || t >= hi[nt][c])) x = -INFINITY;
+            s[bl][nt][k] = x;
+            mx[nt][c] = fmaxf(mx[nt][c], x);
+          }
+      }
+      // the running maxima, and the largest value scale
+      const int e0 = static_cast<int>((__float_as_uint(sc.z) >> 23) & 0xffu);
+      const int e1 = static_cast<int>((__float_as_uint(sc.w) >> 23) & 0xffu);
+      const int E1 = max(E, max(e0, e1));
+      bool grown = E1 > E;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], o));
+          grown |= mx[nt][c] > m[nt][c];
+        }
+      if (__any_sync(0xffffffffu, grown)) {
+        const float de = ex2(static_cast<float>(E - E1));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float nm = fmaxf(m[nt][c], mx[nt][c]);
+            const float a = nm == -INFINITY ? 1.f : ex2(m[nt][c] - nm);
+            m[nt][c] = nm;
+            l[nt][c] *= a;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              acc[i][nt][c] *= a * de;
+              acc[i][nt][2 + c] *= a * de;
+            }
+          }
+        E = E1;
+      }
+      // probabilities, times their block's value scale, as the second product's columns
+      uint32_t pf[W][2][NT][2];
+#pragma unroll
+      for (int bl = 0; bl < 2; ++bl) {
+        const int ev = (bl ? e1 : e0) - E;
+        const float f = ev < -120 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 15 + ev) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float nm = m[nt][k & 1];
+            const float x = ex2(s[bl][nt][k] - (nm == -INFINITY ? 0.f : nm));
+            l[nt][k & 1] += x;
+            w4[k] = x * f;
+          }
+          pf[0][bl][nt][0] = transpose8(pack_h2(w4[0], w4[1]));
+          pf[0][bl][nt][1] = transpose8(pack_h2(w4[2], w4[3]));
+          if constexpr (W == 2) {
+            pf[1][bl][nt][0] = transpose8(pack_h2(h_lo(w4[0]), h_lo(w4[1])));
+            pf[1][bl][nt][1] = transpose8(pack_h2(h_lo(w4[2]), h_lo(w4[3])));
+          }
+        }
+      }
+      // O^T += V^T P^T: lane g holds dims (D / 8) g .. of the four tokens 2 qd, + 1, + 8, + 9
+#pragma unroll
+      for (int bl = 0; bl < 2; ++bl) {
+        constexpr int VW = D / 32;             // words a lane and token
+        uint32_t v4[4][VW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = bl * 16 + 2 * qd + (k & 1) + (k >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 x = lds128(vs_a + swz<D>(row, 16 * g));
+            v4[k][0] = x.x; v4[k][1] = x.y; v4[k][2] = x.z; v4[k][3] = x.w;
+          } else {
+            const uint2 x = lds64(vs_a + swz<D>(row, (8 * g) & ~15) + ((8 * g) & 15));
+            v4[k][0] = x.x; v4[k][1] = x.y;
+          }
+          if (masked)                          // a masked token's NaN stays out of the other rows
+#pragma unroll
+            for (int z = 0; z < VW; ++z) v4[k][z] = e4m3_nan_to_zero(v4[k][z]);
+        }
+#pragma unroll
+        for (int z = 0; z < VW; ++z) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7362u : 0x5140u;
+            const uint32_t x = __byte_perm(v4[0][z], v4[1][z], sel), y = __byte_perm(v4[2][z], v4[3][z], sel);
+            const uint32_t a0 = e4m3x2_to_h2(x), a1 = e4m3x2_to_h2(x >> 16);
+            const uint32_t a2 = e4m3x2_to_h2(y), a3 = e4m3x2_to_h2(y >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[2 * z + half][nt], a0, a1, a2, a3, pf[0][bl][nt][0], pf[0][bl][nt][1]);
+              if constexpr (W == 2)
+                mma_f16(acc[2 * z + half][nt], a0, a1, a2, a3, pf[1][bl][nt][0], pf[1][bl][nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      issue();                                  // into the stage just read
+    }
+
+    // ---- join the warps: common maximum and value scale, then sums in a fixed order
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+        if (g == 0) {
+          s_ml[warp * 33 + nt * 8 + 2 * qd + c] = m[nt][c];
+          s_ml[warp * 33 + 16 + nt * 8 + 2 * qd + c] = l[nt][c];
+        }
+      }
+    if (lane == 0) s_ml[warp * 33 + 32] = static_cast<float>(E);
+    __syncthreads();
+    float Em = 1.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) Em = fmaxf(Em, s_ml[w * 33 + 32]);
+    float M[NT][2], Ls[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * qd + c;
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w * 33 + r]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) ll += s_ml[w * 33 + 16 + r] * ex2(s_ml[w * 33 + r] - ref);
+        M[nt][c] = mm;
+        Ls[nt][c] = ll;
+        const float a = ex2(m[nt][c] - ref + (static_cast<float>(E) - Em));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          acc[i][nt][c] *= a;
+          acc[i][nt][2 + c] *= a;
+        }
+      }
+#pragma unroll
+    for (int half = kWarps / 2; half >= 1; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
+        float* o = s_o + (warp - half) * 8 * NT * D;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * D + (D / 8) * g + 2 * i) =
+                  make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
+      }
+      __syncthreads();
+      if (warp < half) {
+        const float* o = s_o + warp * 8 * NT * D;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float2 x = *reinterpret_cast<const float2*>(o + (nt * 8 + 2 * qd + c) * D + (D / 8) * g + 2 * i);
+              acc[i][nt][c] += x.x;
+              acc[i][nt][2 + c] += x.y;
+            }
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+      const bool whole = sp.tile == 0 && seg_end - u == sp.n;
+      const float unit = ex2(Em - (127.f + 15.f));      // of the accumulated values
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rl = nt * 8 + 2 * qd + c, r = r0 + rl;
+          const float inv = Ls[nt][c] == 0.f ? 0.f : unit / Ls[nt][c];
+          const float ls2 = Ls[nt][c] == 0.f ? -INFINITY : M[nt][c] + __log2f(Ls[nt][c]);
+          if (whole) {
+            if (r < R) {
+              const int i = r / p.G;
+              const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
+              if (p.lse && g == 0) p.lse[row] = ls2 * kLn2;
+#pragma unroll
+              for (int k = 0; k < MT; ++k) {
+                const float x = acc[k][nt][c] * inv, y = acc[k][nt][2 + c] * inv;
+                const int64_t at = row * D + (D / 8) * g + 2 * k;
+                if (W == 2) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
+                else if (p.dtype == TQ_BF16)
+                  *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) = __floats2bfloat162_rn(x, y);
+                else *reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at) = __floats2half2_rn(x, y);
+              }
+            }
+          } else {
+            const int slot = blockIdx.x * 2 + (sp.tile == 0 ? 1 : 0);
+            if (g == 0) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
+            float* o = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + (D / 8) * g;
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+              *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][nt][c] * inv, acc[k][nt][2 + c] * inv);
+          }
+        }
+    }
+    u = seg_end;
+  }
+  // copies still in flight land before the CTA ends (none, unless a wait gave up)
+  for (; used < issued; ++used)
+    for (long long i = 0; !mbar_try(bar0 + 8 * (used % NS), (used / NS) & 1) && i < kDrainLimit; ++i) {}
+}
+
+// Joins the partial results of a (virtual sequence, key head) that several CTAs worked on:
+// out = sum_c w_c out_c / sum_c w_c, w_c = 2^(lse_c - max).  One block a pair; a pair with no
+// visible token gets zeros.
+template <int D>
+__global__ void __launch_bounds__(128) kv8_decode_join_kernel(const Kv8AttnParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int Hkv = p.map.Hkv, v = blockIdx.x / Hkv, h = blockIdx.x - v * Hkv;
+  const int64_t per = __ldg(p.plan);
+  const int t0 = __ldg(p.plan + kPlanHead + v), n = __ldg(p.plan + kPlanHead + v + 1) - t0;
+  const int64_t u = static_cast<int64_t>(t0) * Hkv + static_cast<int64_t>(h) * n;
+  const int c0 = static_cast<int>(u / per), c1 = n ? static_cast<int>((u + n - 1) / per) : c0;
+  if (n && c0 == c1) return;                   // finished where it was computed
+  const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
+  const int R = p.T * p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int PL = D / 32;                   // dims a lane
+  for (int rl = warp; rl < kKv8DecodeRows && r0 + rl < R; rl += 4) {
+    const int r = r0 + rl, i = r / p.G;
+    const int64_t row = (static_cast<int64_t>(b) * p.Hq + h * p.G + (r - i * p.G)) * p.T + i;
+    float mx = -INFINITY, sum = 0.f, o[PL];
+#pragma unroll
+    for (int k = 0; k < PL; ++k) o[k] = 0.f;
+    auto slot_of = [&](int c) { return c * 2 + (c == c0 ? 1 : 0); };
+    if (n) {
+      for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldg(p.part_lse + slot_of(c) * kKv8DecodeRows + rl));
+      mx = warp_max(mx);
+      if (mx > -INFINITY)
+        for (int c = c0; c <= c1; ++c) {
+          const int slot = slot_of(c);
+          const float w = ex2(__ldg(p.part_lse + slot * kKv8DecodeRows + rl) - mx);
+          sum += w;
+          const float* src = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + lane * PL;
+#pragma unroll
+          for (int k = 0; k < PL; ++k) o[k] += w * __ldg(src + k);
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+    const int64_t at = row * D + lane * PL;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+      const float x = o[k] * inv;
+      if (p.dtype == TQ_F32) static_cast<float*>(p.out)[at + k] = x;
+      else if (p.dtype == TQ_BF16) static_cast<__nv_bfloat16*>(p.out)[at + k] = __float2bfloat16_rn(x);
+      else static_cast<__half*>(p.out)[at + k] = __float2half_rn(x);
+    }
+  }
+}
+
+template <int D, int NT, int W>
+cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
+  auto k = kv8_decode_kernel<D, NT, W>;
+  constexpr uint32_t smem = decode_smem(D, NT).total;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, dim3(grid), dim3(kWarps * 32), smem, s, km, vm, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_decode_join_kernel<D>, dim3(static_cast<unsigned>(p.VB) * p.map.Hkv), dim3(128), 0, s, p);
+}
+
+template <int D>
+cudaError_t go_d(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
+  const bool two = p.T * p.G > 8;            // more than one product column block of 8 rows
+  if (p.dtype == TQ_F32) return two ? go<D, 2, 2>(km, vm, p, grid, s) : go<D, 1, 2>(km, vm, p, grid, s);
+  return two ? go<D, 2, 1>(km, vm, p, grid, s) : go<D, 1, 1>(km, vm, p, grid, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
+                              cudaStream_t s) {
+  return d == 128 ? go_d<128>(kmap, vmap, p, grid, s) : go_d<64>(kmap, vmap, p, grid, s);
+}
+
+}  // namespace tq

@@ -1,0 +1,51 @@
+// Launch parameters of the 8-bit cache's kernels (host and device side).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kv8.cuh"
+
+namespace tq {
+
+struct Kv8AppendParams {
+  const void* x[2];                                   // new keys, new values
+  int64_t stride_b[2], stride_h[2], stride_t[2];      // elements
+  int dtype, B, T, blocks;                            // blocks: that T new tokens can touch
+  const int32_t* kv_lens;
+  const int32_t* new_lens;                            // or nullptr: T
+  uint8_t* codes[2];
+  float* scales[2];
+  Kv8Map map;
+  int* status;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t s);
+
+// Attention of B sequences whose query heads share Hkv key heads; rows of a key head are its
+// T * G queries (r = i * G + g), G = Hq / Hkv.
+struct Kv8AttnParams {
+  const void* q;
+  int64_t q_stride_b, q_stride_h, q_stride_t;         // elements
+  int dtype, Hq, G, T;
+  // the launch works on virtual sequences v0 .. v0 + VB - 1; sequence v / RG, row group v % RG
+  int v0, VB, RG;
+  const float* kscales;
+  const float* vscales;
+  Kv8Scoring sc;
+  Kv8Map map;
+  void* out;                                          // [B][Hq][T][d], dtype
+  float* lse;                                         // [B][Hq][T] or nullptr
+  float* part_o;                                      // partial results of split rows
+  float* part_lse;
+  int* plan;                                          // how the launch's work is split
+  int* status;
+  long long wait_limit;
+};
+// Groups of 16 rows a key head (decode; fp32 queries).  kmap / vmap: the codes as [records][d]
+// bytes in boxes of 16 rows.
+constexpr int kKv8DecodeRows = 16;
+constexpr int kKv8DecodeMaxVB = 1024;                 // virtual sequences a launch
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
+                              cudaStream_t s);
+
+}  // namespace tq

@@ -1,0 +1,402 @@
+// Pages of a cache: reference counts, allocation, forks, compaction and the copies they need.
+//
+// A page is free while its count is 0.  Allocation takes the free pages of the lowest ids in the
+// order of the requests, so a call's result depends on its arguments alone; there is no free list
+// to keep in step.  Ranks of free (or live) pages come from counts of chunks of 4096 pages, then
+// from a scan inside the chunk.  A call that cannot be served whole (too few free pages, a bad or
+// repeated row) changes nothing: the kernel that would change something first sees the counts of
+// all chunks and the verdict on all requests, which the kernel before it wrote.
+//
+// The bookkeeping reads 4 bytes a page and is bound by launch and memory latency; the copies are
+// bound by bytes, 2 a byte moved, and go in slices of 16 KB with four 16-byte loads in flight a
+// thread.
+#include "pages.h"
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "launchers.h"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = kPageChunk / kThreads;  // counts a thread
+
+// Sum over the block; every thread gets it.
+__device__ __forceinline__ int block_sum(int x, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if (lane == 0) sh[warp] = x;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
+  return t;
+}
+
+// Sum over the threads before this one.
+__device__ __forceinline__ int block_before(int x, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = s;
+  __syncthreads();
+  int t = s - x;
+  for (int w = 0; w < warp; ++w) t += sh[w];
+  return t;
+}
+
+__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+
+// Counts of this thread's pages p0 .. p0 + kPer - 1 (pages past the pool count as live).
+__device__ __forceinline__ void load_refs(const tq_page_pool& pool, int64_t p0, int (&r)[kPer]) {
+  if (p0 + kPer <= pool.num_pages) {
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(pool.refs + p0 + k);
+      r[k] = v.x; r[k + 1] = v.y; r[k + 2] = v.z; r[k + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) r[k] = p0 + k < pool.num_pages ? pool.refs[p0 + k] : 1;
+  }
+}
+
+__device__ __forceinline__ int count_free(const int (&r)[kPer]) {
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) n += r[k] <= 0;
+  return n;
+}
+
+// Marks row `r` of bitmap `m`; true if it was marked before.
+__device__ __forceinline__ bool mark(uint32_t* m, int r) {
+  const uint32_t bit = 1u << (r & 31);
+  return atomicOr(m + (r >> 5), bit) & bit;
+}
+
+// The last block: what the requests want, and whether they can be served at all.
+template <bool FORK>
+__device__ void scan_requests(const PagesParams& p, int* sh) {
+  __shared__ int bad;
+  const int words = (p.pool.rows + 31) / 32, cap = p.pool.max_pages * p.pool.page_size;
+  if (threadIdx.x == 0) bad = 0;
+  for (int i = threadIdx.x; i < 2 * words; i += kThreads) p.marks[i] = 0;
+  __syncthreads();
+  int run = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    int want = 0;
+    if (i < p.n) {
+      const int row = p.rows[i], len = p.lens[i];
+      bool ok = row >= 0 && row < p.pool.rows && len >= 0 && len <= cap;
+      if (FORK) {
+        const int src = p.src[i];
+        ok = ok && src >= 0 && src < p.pool.rows;
+        if (ok) {
+          mark(p.marks + words, src);
+          want = len % p.pool.page_size ? 1 : 0;
+        }
+      } else {
+        const int old = p.old_lens[i];
+        ok = ok && old >= 0 && old <= cap;
+        if (ok) want = max(0, pages_of(len, p.pool.page_size) - pages_of(old, p.pool.page_size));
+      }
+      if (!ok || mark(p.marks, row)) atomicOr(&bad, 1);
+    }
+    const int before = block_before(want, sh);
+    if (i < p.n) p.prefix[i] = run + before;
+    run += block_sum(want, sh);
+  }
+  __syncthreads();
+  if (FORK)                                  // a row that is made must not be copied from too
+    for (int i = threadIdx.x; i < words; i += kThreads)
+      if (p.marks[i] & p.marks[words + i]) atomicOr(&bad, 1);
+  __syncthreads();
+  if (threadIdx.x == 0) p.prefix[p.n] = bad ? -1 : run;
+}
+
+enum : int { COUNT_FORK = 0, COUNT_RESERVE = 1, COUNT_COMPACT = 2 };
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p) {
+  __shared__ int sh[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  if (MODE != COUNT_COMPACT && static_cast<int>(blockIdx.x) == p.chunks) {
+    scan_requests<MODE == COUNT_FORK>(p, sh);
+    return;
+  }
+  int r[kPer];
+  load_refs(p.pool, static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPer, r);
+  const int n = block_sum(count_free(r), sh);
+  if (threadIdx.x == 0) p.chunk_free[blockIdx.x] = n;
+}
+
+// Free pages of the chunks before `chunk`, and of all.
+__device__ __forceinline__ void chunk_sums(const PagesParams& p, int chunk, int* sh, int& before, int& all) {
+  int b = 0, a = 0;
+  for (int c = threadIdx.x; c < p.chunks; c += kThreads) {
+    const int n = p.chunk_free[c];
+    a += n;
+    if (c < chunk) b += n;
+  }
+  before = block_sum(b, sh);
+  all = block_sum(a, sh);
+}
+
+// Blocks 0 .. chunks - 1 hand out the free pages of their chunk; fork has one more block a
+// request, which shares the parent's whole pages.
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
+  __shared__ int sh[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const tq_page_pool& pool = p.pool;
+  const int need = p.prefix[p.n];
+  int before, all;
+  chunk_sums(p, blockIdx.x, sh, before, all);
+  const bool short_of = need < 0 || all < need;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.shortfall = need < 0 ? -1 : max(0, need - all);
+    if (need < 0) report_status(p.status, TQ_ERR_INVALID_ARG);
+  }
+  if (FORK && static_cast<int>(blockIdx.x) >= p.chunks) {
+    const int i = blockIdx.x - p.chunks;
+    const int len = p.lens[i];
+    if (short_of) {
+      if (threadIdx.x == 0) p.to[i] = -1;
+      return;
+    }
+    const int full = len / pool.page_size;
+    const int32_t* from = pool.block_table + static_cast<int64_t>(p.src[i]) * pool.max_pages;
+    int32_t* to = pool.block_table + static_cast<int64_t>(p.rows[i]) * pool.max_pages;
+    for (int c = threadIdx.x; c < full; c += kThreads) {
+      const int id = from[c];
+      to[c] = id;
+      if (id >= 0 && id < pool.num_pages) atomicAdd(pool.refs + id, 1);
+      else report_status(p.status, TQ_ERR_INVALID_ARG);
+    }
+    if (threadIdx.x == 0) {
+      int id = -1;
+      if (len % pool.page_size) {
+        id = from[full];
+        if (id < 0 || id >= pool.num_pages) {
+          report_status(p.status, TQ_ERR_INVALID_ARG);
+          id = -1;
+        }
+      }
+      p.from[i] = id;
+      if (len % pool.page_size == 0) p.to[i] = -1;
+    }
+    return;
+  }
+  if (short_of || before >= need) return;
+  int r[kPer];
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kPageChunk + threadIdx.x * kPer;
+  load_refs(pool, p0, r);
+  int rank = before + block_before(count_free(r), sh);
+#pragma unroll 1
+  for (int k = 0; k < kPer && rank < need; ++k) {
+    if (r[k] > 0) continue;
+    int lo = 0, hi = p.n - 1;                // the request that wants page `rank`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.prefix[mid] <= rank) lo = mid; else hi = mid - 1;
+    }
+    const int id = static_cast<int>(p0 + k);
+    const int col = FORK ? p.lens[lo] / pool.page_size : pages_of(p.old_lens[lo], pool.page_size) + rank - p.prefix[lo];
+    pool.block_table[static_cast<int64_t>(p.rows[lo]) * pool.max_pages + col] = id;
+    pool.refs[id] = 1;
+    if (FORK) p.to[lo] = id;
+    ++rank;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) free_kernel(const PagesParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const tq_page_pool& pool = p.pool;
+  const int i = blockIdx.x, row = p.rows[i], cap = pool.max_pages * pool.page_size;
+  int len = p.lens[i];
+  if (row < 0 || row >= pool.rows || len < 0 || len > cap) {
+    if (threadIdx.x == 0) report_status(p.status, TQ_ERR_INVALID_ARG);
+    return;
+  }
+  const int used = pages_of(len, pool.page_size);
+  for (int c = threadIdx.x; c < used; c += kThreads) {
+    // a row that is named twice gives its pages back once
+    const int id = atomicExch(pool.block_table + static_cast<int64_t>(row) * pool.max_pages + c, -1);
+    if (id == -1) continue;
+    if (id < 0 || id >= pool.num_pages) {
+      report_status(p.status, TQ_ERR_INVALID_ARG);
+    } else if (atomicSub(pool.refs + id, 1) <= 0) {
+      atomicAdd(pool.refs + id, 1);          // it was free already
+      report_status(p.status, TQ_ERR_INVALID_ARG);
+    }
+  }
+}
+
+// Compaction, pass 2: with L live pages, the live ones at ids >= L move, in their order, to the
+// free ids below L in theirs.  map: own id, -1 (free), or -2 - j for the j-th page that moves.
+__global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PagesParams p) {
+  __shared__ int sh[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const tq_page_pool& pool = p.pool;
+  int before, all;
+  chunk_sums(p, blockIdx.x, sh, before, all);
+  const int64_t L = pool.num_pages - all;    // live pages
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.live = static_cast<int>(L);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kPageChunk, p0 = c0 + threadIdx.x * kPer;
+  // free pages below L: those of the chunks before L's, and of the part of L's chunk
+  int low_free = 0;
+  if (c0 + kPageChunk > L) {
+    const int lc = static_cast<int>(min(L / kPageChunk, static_cast<int64_t>(p.chunks)));
+    int n = 0;
+    for (int c = threadIdx.x; c < lc; c += kThreads) n += p.chunk_free[c];
+    for (int64_t q = static_cast<int64_t>(lc) * kPageChunk + threadIdx.x; q < L; q += kThreads) n += pool.refs[q] <= 0;
+    low_free = block_sum(n, sh);
+  }
+  int r[kPer];
+  load_refs(pool, p0, r);
+  int frank = before + block_before(count_free(r), sh);       // free pages before p0
+#pragma unroll 1
+  for (int k = 0; k < kPer && p0 + k < pool.num_pages; ++k) {
+    const int64_t id = p0 + k;
+    int m = -1;
+    if (r[k] > 0) {
+      m = static_cast<int>(id);
+      if (id >= L) {
+        const int j = static_cast<int>(id - frank - (L - low_free));
+        p.from[j] = static_cast<int>(id);
+        m = -2 - j;
+      }
+    } else {
+      if (id < L) p.to[frank] = static_cast<int>(id);
+      ++frank;
+    }
+    p.page_map[id] = m;
+  }
+}
+
+template <typename V, int N>
+__device__ __forceinline__ void copy_units(V* dst, const V* src, int units) {
+  int i = threadIdx.x;
+  for (; i + (N - 1) * kThreads < units; i += N * kThreads) {
+    V v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __ldcs(src + i + k * kThreads);
+#pragma unroll
+    for (int k = 0; k < N; ++k) __stcs(dst + i + k * kThreads, v[k]);
+  }
+  for (; i < units; i += kThreads) dst[i] = src[i];
+}
+
+enum : int { COPY_LIST = 0, COPY_FORK = 1, COPY_COMPACT = 2 };
+
+// Moves the pages of the pairs in from / to, one slice of one array a step.
+template <int MODE>
+__global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n_pages = p.pool.num_pages;
+  int64_t pairs = p.n;
+  if (MODE == COPY_COMPACT) {
+    // pages that move: free pages below the live count
+    __shared__ int sh[kThreads / 32];
+    const int64_t L = *p.live;
+    const int lc = static_cast<int>(L / kPageChunk);
+    int n = 0;
+    for (int c = threadIdx.x; c < lc; c += kThreads) n += p.chunk_free[c];
+    for (int64_t q = static_cast<int64_t>(lc) * kPageChunk + threadIdx.x; q < L; q += kThreads) {
+      // the counts are being moved by other blocks; the map is not, for pages below L
+      n += p.page_map[q] == -1;
+    }
+    pairs = block_sum(n, sh);
+    // entries of the table, by the map (-2 - j: the page that pair j leads to)
+    const int64_t entries = static_cast<int64_t>(p.pool.rows) * p.pool.max_pages;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < entries;
+         e += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int id = p.pool.block_table[e];
+      if (id < 0) continue;
+      if (id >= n_pages) { report_status(p.status, TQ_ERR_INVALID_ARG); continue; }
+      int m = *static_cast<volatile int32_t*>(p.page_map + id);
+      if (m <= -2) m = p.to[-2 - m];
+      if (m != id) p.pool.block_table[e] = m;
+    }
+  }
+  const int slices = p.copy.slice0[p.copy.n];
+  for (int64_t w = blockIdx.x; w < pairs * slices; w += gridDim.x) {
+    const int64_t j = w / slices;
+    const int s = static_cast<int>(w - j * slices);
+    int from, to;
+    if (MODE == COPY_LIST) { from = p.src[j]; to = p.rows[j]; }
+    else { to = p.to[j]; from = MODE == COPY_FORK && to < 0 ? -1 : p.from[j]; }
+    if (MODE == COPY_FORK && (to < 0 || from < 0)) continue;
+    if (from < 0 || from >= n_pages || to < 0 || to >= n_pages) {
+      if (threadIdx.x == 0) report_status(p.status, TQ_ERR_INVALID_ARG);
+      continue;
+    }
+    if (MODE == COPY_COMPACT && s == 0 && threadIdx.x == 0) {
+      p.pool.refs[to] = p.pool.refs[from];
+      p.pool.refs[from] = 0;
+      *static_cast<volatile int32_t*>(p.page_map + from) = to;
+    }
+    if (from == to) continue;
+    int a = 0;
+    while (s >= p.copy.slice0[a + 1]) ++a;
+    const int64_t pb = p.copy.page_bytes[a], off = static_cast<int64_t>(s - p.copy.slice0[a]) * kCopySlice;
+    const int bytes = static_cast<int>(min(pb - off, static_cast<int64_t>(kCopySlice)));
+    char* dst = p.copy.data[a] + to * pb + off;
+    const char* src = p.copy.data[a] + from * pb + off;
+    if (pb % 16 == 0) copy_units<uint4, 4>(reinterpret_cast<uint4*>(dst), reinterpret_cast<const uint4*>(src), bytes / 16);
+    else copy_units<uint32_t, 4>(reinterpret_cast<uint32_t*>(dst), reinterpret_cast<const uint32_t*>(src), bytes / 4);
+  }
+}
+
+// Blocks of a copy: all slices where they are few, else eight an SM.
+unsigned copy_grid(int64_t pairs, const PagesParams& p, int sms) {
+  const int64_t all = pairs * p.copy.slice0[p.copy.n];
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(all, 8ll * sms)));
+}
+
+}  // namespace
+
+cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t s) {
+  return launch_pdl(free_kernel, dim3(p.n), dim3(kThreads), 0, s, p);
+}
+
+cudaError_t launch_pages_reserve(const PagesParams& p, cudaStream_t s) {
+  cudaError_t e = launch_pdl(count_kernel<COUNT_RESERVE>, dim3(p.chunks + 1), dim3(kThreads), 0, s, p);
+  return e != cudaSuccess ? e : launch_pdl(assign_kernel<false>, dim3(p.chunks), dim3(kThreads), 0, s, p);
+}
+
+cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t s) {
+  cudaError_t e = launch_pdl(count_kernel<COUNT_FORK>, dim3(p.chunks + 1), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(assign_kernel<true>, dim3(p.chunks + p.n), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(copy_kernel<COPY_FORK>, dim3(copy_grid(p.n, p, sms)), dim3(kThreads), 0, s, p);
+  return e;
+}
+
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t s) {
+  cudaError_t e = launch_pdl(count_kernel<COUNT_COMPACT>, dim3(p.chunks), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(compact_plan_kernel, dim3(p.chunks), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(copy_kernel<COPY_COMPACT>, dim3(copy_grid(p.pool.num_pages / 2 + 1, p, sms)), dim3(kThreads), 0, s, p);
+  return e;
+}
+
+cudaError_t launch_pages_copy(const PagesParams& p, int sms, cudaStream_t s) {
+  return launch_pdl(copy_kernel<COPY_LIST>, dim3(copy_grid(p.n, p, sms)), dim3(kThreads), 0, s, p);
+}
+
+}  // namespace tq

@@ -55,18 +55,11 @@ long long wait_limit() {
   return v != 0 ? v : kDefaultWaitLimit;
 }
 
-namespace {
-
-tq_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+tq_status cuda_fail(int e, const char* what) {
+  return fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(static_cast<cudaError_t>(e)));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  const void* p;
-  size_t bytes;
-};
+namespace {
 
 bool overlaps(Range a, Range b) {
   if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
@@ -74,13 +67,15 @@ bool overlaps(Range a, Range b) {
   return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 
-size_t dtype_size(int dtype) { return dtype == TQ_F32 ? 4 : 2; }
+}  // namespace
 
 int sm_count() {
   int dev = 0, n = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   return n > 0 ? n : 148;
 }
+
+namespace {
 
 int spectral_head_bits(const tq_quantizer* q) {
   int s = 0;
@@ -158,6 +153,8 @@ void packed_ranges(const tq_packed& pk, const tq_layout& L, int64_t n, Range out
   out[3] = {L.has_rnorms ? pk.rnorms : nullptr, static_cast<size_t>(n) * 4};
 }
 
+}  // namespace
+
 tq_status check_no_alias(const Range* outs, int nout, const Range* ins, int nin) {
   for (int i = 0; i < nout; ++i) {
     for (int j = 0; j < nin; ++j)
@@ -167,6 +164,8 @@ tq_status check_no_alias(const Range* outs, int nout, const Range* ins, int nin)
   }
   return TQ_OK;
 }
+
+namespace {
 
 // ---- tensor map for the tensor-core quantize ----
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
@@ -545,6 +544,8 @@ struct DecodeCall {
   int T;
 };
 
+}  // namespace
+
 tq_status check_pages(const tq_pages* pg) {
   if (!pg || !pg->block_table) return fail(TQ_ERR_INVALID_ARG, "pages or block_table is NULL");
   if (!aligned16(pg->block_table)) return fail(TQ_ERR_ALIGNMENT, "block_table not 16-byte aligned");
@@ -555,6 +556,22 @@ tq_status check_pages(const tq_pages* pg) {
   if (pg->num_pages > (1ll << 31) - 1) return fail(TQ_ERR_INVALID_ARG, "num_pages too large");
   return TQ_OK;
 }
+
+tq_status byte_rows_map(void* map, const void* ptr, int64_t rows, int cols, int box_rows) {
+  auto enc = get_encode();
+  if (!enc) return fail(TQ_ERR_CUDA, "cuTensorMapEncodeTiled not available");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows)}, ones[2] = {1, 1};
+  if (enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
+          ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(TQ_ERR_CUDA, "tensor map encode failed");
+  return TQ_OK;
+}
+
+namespace {
 
 tq_status decode_run(const DecodeCall& c) {
   const tq_quantizer* kq = c.kq;

@@ -25,6 +25,21 @@ tq_status spectral_descriptor(const double* vecs, const double* vals, int d, int
 // The shape and descriptor checks tq_decode_attn runs before anything else (tq_api.cu).
 tq_status decode_shape_ok(const tq_quantizer* kq, const tq_quantizer* vq, int B, int Hq, int Hkv, int64_t Nmax);
 
+// Argument checks shared by the entry points (tq_api.cu).
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t dtype_size(int dtype) { return dtype == TQ_F32 ? 4 : 2; }
+tq_status check_no_alias(const Range* outs, int nout, const Range* ins, int nin);
+tq_status check_pages(const tq_pages* pg);
+tq_status cuda_fail(int cuda_error, const char* what);
+int sm_count();                // of the current device
+// Tensor map of a byte matrix [rows][cols], boxes of box_rows whole rows, rows swizzled by their
+// own width (64 or 128 bytes); map: CUtensorMap* (tq_api.cu).
+tq_status byte_rows_map(void* map, const void* ptr, int64_t rows, int cols, int box_rows);
+
 // Device-side status word and wait limit (tq_api.cu).
 int* device_status_ptr();      // address of the current device's status word
 long long wait_limit();        // polls per bounded wait

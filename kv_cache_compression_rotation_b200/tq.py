@@ -34,7 +34,8 @@ EXPORTS = [
     "tq_decode_attn_fixed_ws", "tq_quantize_split", "tq_score_split_workspace", "tq_score_split",
     "tq_decode_attn_split_workspace", "tq_decode_attn_split", "tq_spectral_descriptor", "tq_spectral_prepare",
     "tq_decode_attn_paged", "tq_prefill_attn_workspace", "tq_prefill_attn", "tq_quantize_workspace",
-    "tq_quantize_ws",
+    "tq_quantize_ws", "tq_kv8_append", "tq_kv8_attn_workspace", "tq_kv8_decode_attn", "tq_kv8_prefill_attn",
+    "tq_pages_workspace", "tq_pages_free", "tq_pages_reserve", "tq_pages_fork", "tq_pages_compact", "tq_pages_copy",
 ]
 
 
@@ -70,6 +71,32 @@ class Split_t(C.Structure):
 class Pages_t(C.Structure):
     _fields_ = [("block_table", C.c_void_p), ("page_size", C.c_int32), ("max_pages", C.c_int32),
                 ("num_pages", C.c_int64)]
+
+
+class Kv8_t(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
+class Strides_t(C.Structure):
+    _fields_ = [("b", C.c_int64), ("h", C.c_int64), ("t", C.c_int64)]
+
+
+class Scoring_t(C.Structure):
+    _fields_ = [("scale", C.c_float), ("softcap", C.c_float), ("slopes", C.c_void_p), ("window", C.c_int32),
+                ("first", C.c_void_p), ("prefix", C.c_void_p)]
+
+
+class PagePool_t(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("refs", C.c_void_p), ("rows", C.c_int32), ("max_pages", C.c_int32),
+                ("page_size", C.c_int32), ("num_pages", C.c_int64)]
+
+
+class PoolArray_t(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_bytes", C.c_int64)]
+
+
+KV8_BLOCK = 16
+MAX_POOL_ARRAYS = 16
 
 
 class Layout_t(C.Structure):
@@ -132,6 +159,23 @@ def lib():
             "tq_decode_attn_split": ([C.POINTER(Split_t), C.POINTER(Split_t), vp, i32, i32, i32, i32, i64, vp,
                                       C.POINTER(Packed_t), C.POINTER(Packed_t), C.c_float, vp, vp, C.c_size_t,
                                       vp], C.c_int),
+            "tq_kv8_append": ([vp, vp, i32, C.POINTER(Strides_t), C.POINTER(Strides_t), i32, i32, i32, i32, vp, vp,
+                               C.POINTER(Pages_t), i64, Kv8_t, Kv8_t, vp], C.c_int),
+            "tq_kv8_attn_workspace": ([i32, i32, i32, i32, i32, i32, i64, C.POINTER(C.c_size_t)], C.c_int),
+            "tq_kv8_decode_attn": ([vp, C.POINTER(Strides_t), i32, i32, i32, i32, i32, vp, C.POINTER(Scoring_t),
+                                    C.POINTER(Pages_t), i64, vp, vp, C.POINTER(Strides_t), C.POINTER(Strides_t), Kv8_t,
+                                    Kv8_t, vp, vp, vp, C.c_size_t, vp], C.c_int),
+            "tq_kv8_prefill_attn": ([vp, C.POINTER(Strides_t), i32, i32, i32, i32, i32, i32, vp, vp,
+                                     C.POINTER(Scoring_t), C.POINTER(Pages_t), i64, Kv8_t, Kv8_t, vp, vp, vp,
+                                     C.c_size_t, vp], C.c_int),
+            "tq_pages_workspace": ([C.POINTER(PagePool_t), i32, C.POINTER(C.c_size_t)], C.c_int),
+            "tq_pages_free": ([C.POINTER(PagePool_t), vp, vp, i32, vp], C.c_int),
+            "tq_pages_reserve": ([C.POINTER(PagePool_t), vp, vp, vp, i32, vp, vp, C.c_size_t, vp], C.c_int),
+            "tq_pages_fork": ([C.POINTER(PagePool_t), C.POINTER(PoolArray_t), i32, vp, vp, vp, i32, vp, vp, C.c_size_t,
+                               vp], C.c_int),
+            "tq_pages_compact": ([C.POINTER(PagePool_t), C.POINTER(PoolArray_t), i32, vp, vp, vp, C.c_size_t, vp],
+                                 C.c_int),
+            "tq_pages_copy": ([C.POINTER(PoolArray_t), i32, i64, vp, vp, i32, vp], C.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -547,6 +591,289 @@ def prefill_attn(kq: Quantizer, vq: Quantizer, q, q_pos, kv_lens, kcache: Packed
                                  vcache.as_c(), float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                  _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ 8-bit block-scaled cache
+class Kv8:
+    """One side of an 8-bit cache: codes uint8 [records, d] (e4m3 bytes) and scales fp32
+    [records / 16] (CUDA tensors)."""
+
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or scales.dtype is not torch.float32:
+            raise ValueError("codes must be uint8 or float8_e4m3fn and scales float32")
+        if codes.dim() != 2 or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes [records, d] and scales must be contiguous")
+        if scales.numel() * KV8_BLOCK != codes.shape[0]:
+            raise ValueError(f"scales must hold one value for each {KV8_BLOCK} of the {codes.shape[0]} records")
+        self.codes, self.scales, self.d, self.records = codes, scales, codes.shape[1], codes.shape[0]
+        self.device = codes.device
+        self.c = Kv8_t(codes.data_ptr(), scales.data_ptr())
+
+
+def kv8_alloc(records: int, d: int, device="cuda") -> Kv8:
+    """A zeroed side of `records` records (a multiple of 16)."""
+    import torch
+    return Kv8(torch.zeros((records, d), dtype=torch.uint8, device=device),
+               torch.zeros(records // KV8_BLOCK, dtype=torch.float32, device=device))
+
+
+class Scoring:
+    """Options of the 8-bit attention's scores (tq_scoring): scale (default 1/sqrt(d)), softcap,
+    slopes fp32 [Hq], window, first int32 [B, T] (document starts), prefix int32 [B]."""
+
+    def __init__(self, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, window: int = 0, first=None,
+                 prefix=None):
+        import torch
+        for name, t, dt in (("slopes", slopes, torch.float32), ("first", first, torch.int32),
+                            ("prefix", prefix, torch.int32)):
+            if t is not None and (t.dtype is not dt or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor")
+        self.scale, self.slopes, self.first, self.prefix = scale, slopes, first, prefix
+        self.by_d = {}
+        self.softcap, self.window = float(softcap), int(window)
+
+    def as_c(self, d: int):
+        c = self.by_d.get(d)
+        if c is None:
+            c = Scoring_t(1.0 / math.sqrt(d) if self.scale is None else float(self.scale), self.softcap,
+                          _dptr(self.slopes), self.window, _dptr(self.first), _dptr(self.prefix))
+            self.by_d[d] = c
+        return c
+
+    def check(self, B: int, Hq: int, T: int) -> None:
+        for name, t, n in (("slopes", self.slopes, Hq), ("first", self.first, B * T), ("prefix", self.prefix, B)):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{name} must hold {n} values (got {t.numel()})")
+
+
+def _ints(t, n: int, name: str):
+    import torch
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, d: int):
+    if t.stride(-1) != 1 or t.shape[-1] != d:
+        raise ValueError(f"{name}: the last dimension must be {d} contiguous elements")
+    return t.data_ptr()
+
+
+def _same_device(device, *ts):
+    import torch
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device} in one call")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device (got {device})")
+
+
+def _kv8_cache(kcache: Kv8, vcache: Kv8, B: int, Hkv: int, Nmax: int, pages):
+    """Checks that the sides hold what the layout addresses; returns the capacity in tokens."""
+    if kcache.d != vcache.d or kcache.records != vcache.records:
+        raise ValueError("kcache and vcache differ in shape")
+    need = pages.records(Hkv) if pages is not None else B * Hkv * Nmax
+    if need > kcache.records:
+        raise ValueError(f"the cache holds {kcache.records} records, the layout addresses {need}")
+    if pages is not None:
+        if pages.block_table.shape[0] < B or pages.block_table.element_size() != 4:
+            raise ValueError(f"block_table must be int32 with a row for each of {B} sequences")
+        return pages.max_pages * pages.page_size
+    return Nmax
+
+
+def kv8_append(kcache: Kv8, vcache: Kv8, k_new, v_new, kv_lens, new_lens=None, Nmax: int = 0,
+               pages: Optional[Pages] = None, stream=None) -> None:
+    """tq_kv8_append: k_new / v_new [B, Hkv, T, d] (any strides, d contiguous) become the last tokens
+    of each sequence; kv_lens int32 [B] counts them, new_lens int32 [B] says how many of the T."""
+    B, Hkv, T, d = k_new.shape
+    if v_new.shape != k_new.shape or v_new.dtype is not k_new.dtype or kcache.d != d:
+        raise ValueError("k_new, v_new and the cache differ in shape or dtype")
+    _same_device(k_new.device, v_new, kv_lens, new_lens, kcache.codes, vcache.codes)
+    _kv8_cache(kcache, vcache, B, Hkv, Nmax, pages)
+    ks, vs = k_new.stride(), v_new.stride()
+    _check(lib().tq_kv8_append(_rows(k_new, "k_new", d), _rows(v_new, "v_new", d), _dtype_code(k_new),
+                               C.byref(Strides_t(ks[0], ks[1], ks[2])), C.byref(Strides_t(vs[0], vs[1], vs[2])), B, Hkv,
+                               T, d, _ints(kv_lens, B, "kv_lens"),
+                               None if new_lens is None else _ints(new_lens, B, "new_lens"),
+                               None if pages is None else pages.ref, Nmax, kcache.c, vcache.c, _stream(stream)))
+
+
+def kv8_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, T: int, d: int, Nmax: int) -> int:
+    """Workspace of the 8-bit attention calls (T = 1: decode); dtype as a torch dtype."""
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
+    ws = C.c_size_t(0)
+    _check(lib().tq_kv8_attn_workspace(code, B, Hq, Hkv, T, d, Nmax, C.byref(ws)))
+    return ws.value
+
+
+_PLAIN_SCORING = Scoring()
+
+
+def _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring):
+    cap = _kv8_cache(kcache, vcache, B, Hkv, Nmax, pages)
+    if kcache.d != d:
+        raise ValueError(f"q has d = {d}, the cache {kcache.d}")
+    scoring = _PLAIN_SCORING if scoring is None else scoring
+    scoring.check(B, Hq, T)
+    return cap, scoring
+
+
+def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0, pages: Optional[Pages] = None,
+                    k_new=None, v_new=None, scoring: Optional[Scoring] = None, out=None, lse=None,
+                    return_lse: bool = False, workspace=None, stream=None):
+    """tq_kv8_decode_attn: one step for q [B, Hq, d], output of q's dtype (with lse fp32 [B, Hq] when
+    return_lse); k_new / v_new [B, Hkv, d] are appended as token kv_lens[b] - 1 first."""
+    B, Hq, d = q.shape
+    cap, scoring = _kv8_attn_checks(B, Hq, 1, d, kcache, vcache, Hkv, Nmax, pages, scoring)
+    _same_device(q.device, kv_lens, kcache.codes, vcache.codes, k_new, v_new, out, lse, workspace, scoring.slopes,
+                 scoring.first, scoring.prefix)
+    kst = vst = None
+    if k_new is not None:
+        if v_new is None or k_new.shape != (B, Hkv, d) or v_new.shape != (B, Hkv, d) or \
+                k_new.dtype is not q.dtype or v_new.dtype is not q.dtype:
+            raise ValueError(f"k_new and v_new must be [{B}, {Hkv}, {d}] of q's dtype")
+        kst, vst = (C.byref(Strides_t(t.stride(0), t.stride(1), 0)) for t in (k_new, v_new))
+    out, lse, ws = _kv8_outputs(q, (B, Hq, d), out, lse, return_lse, workspace, B, Hq, Hkv, 1, d, cap)
+    _check(lib().tq_kv8_decode_attn(_rows(q, "q", d), C.byref(Strides_t(q.stride(0), q.stride(1), 0)), _dtype_code(q), B,
+                                    Hq, Hkv, d, _ints(kv_lens, B, "kv_lens"), C.byref(scoring.as_c(d)),
+                                    None if pages is None else pages.ref, Nmax,
+                                    None if k_new is None else _rows(k_new, "k_new", d),
+                                    None if v_new is None else _rows(v_new, "v_new", d), kst, vst, kcache.c, vcache.c,
+                                    out.data_ptr(), _dptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def _kv8_outputs(q, shape, out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap):
+    import torch
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(shape)}")
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    elif lse.shape != shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape[:-1])}")
+    if workspace is None:
+        workspace = torch.empty(kv8_workspace_bytes(q.dtype, B, Hq, Hkv, T, d, cap), dtype=torch.uint8, device=q.device)
+    return out, lse, workspace
+
+
+def kv8_prefill_attn(q, q_pos, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0,
+                     pages: Optional[Pages] = None, scoring: Optional[Scoring] = None, out=None, lse=None,
+                     return_lse: bool = False, workspace=None, stream=None):
+    """tq_kv8_prefill_attn: q [B, Hq, T, d] (any strides, d contiguous) at positions q_pos int32 [B, T]
+    over the 8-bit cache; output [B, Hq, T, d] of q's dtype (with lse fp32 [B, Hq, T] when return_lse)."""
+    B, Hq, T, d = q.shape
+    cap, scoring = _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring)
+    _same_device(q.device, q_pos, kv_lens, kcache.codes, vcache.codes, out, lse, workspace, scoring.slopes,
+                 scoring.first, scoring.prefix)
+    out, lse, ws = _kv8_outputs(q, (B, Hq, T, d), out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap)
+    st = q.stride()
+    _check(lib().tq_kv8_prefill_attn(_rows(q, "q", d), C.byref(Strides_t(st[0], st[1], st[2])), _dtype_code(q), B, Hq, Hkv,
+                                     T, d, _ints(q_pos, B * T, "q_pos"), _ints(kv_lens, B, "kv_lens"),
+                                     C.byref(scoring.as_c(d)), None if pages is None else pages.ref, Nmax, kcache.c,
+                                     vcache.c, out.data_ptr(), _dptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ page pool
+class PagePool:
+    """Which pages each row (sequence) of a paged cache holds: block_table int32 [rows, max_pages],
+    refs int32 [num_pages] (counts, 0 = free), and the record arrays whose pages move together
+    (Packed or Kv8 arrays: [num_pages * Hkv * page_size, ...] tensors)."""
+
+    def __init__(self, block_table, refs, page_size: int, arrays=()):
+        import torch
+        for name, t in (("block_table", block_table), ("refs", refs)):
+            if t.dtype is not torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor")
+        self.block_table, self.refs, self.page_size, self.arrays = block_table, refs, page_size, list(arrays)
+        self.rows, self.max_pages = block_table.shape
+        self.num_pages = refs.numel()
+        self.device = block_table.device
+        if len(self.arrays) > MAX_POOL_ARRAYS:
+            raise ValueError(f"at most {MAX_POOL_ARRAYS} arrays")
+        pa = (PoolArray_t * max(1, len(self.arrays)))()
+        for i, a in enumerate(self.arrays):
+            nbytes = a.numel() * a.element_size()
+            if not a.is_contiguous() or nbytes % self.num_pages or a.device != self.device:
+                raise ValueError(f"array {i} must be contiguous, on {self.device}, and a whole number of bytes a page")
+            pa[i] = PoolArray_t(a.data_ptr(), nbytes // self.num_pages)
+        self.pa = pa
+        self.c = PagePool_t(block_table.data_ptr(), refs.data_ptr(), self.rows, self.max_pages, page_size,
+                            self.num_pages)
+
+    def pages(self) -> Pages:
+        """The pool's block table as the paged calls take it (row b = sequence b)."""
+        return Pages(self.block_table, self.page_size, self.num_pages)
+
+    def _work(self, n: int):
+        import torch
+        ws = C.c_size_t(0)
+        _check(lib().tq_pages_workspace(C.byref(self.c), n, C.byref(ws)))
+        return torch.empty(ws.value, dtype=torch.uint8, device=self.device)
+
+
+def _one_int(pool: PagePool):
+    import torch
+    return torch.empty(1, dtype=torch.int32, device=pool.device)
+
+
+def pages_free(pool: PagePool, rows, lens, stream=None) -> None:
+    """tq_pages_free: rows int32 [n] give back the pages of their first lens int32 [n] tokens."""
+    n = rows.numel()
+    _same_device(pool.device, rows, lens)
+    _check(lib().tq_pages_free(C.byref(pool.c), _ints(rows, n, "rows"), _ints(lens, n, "lens"), n, _stream(stream)))
+
+
+def pages_reserve(pool: PagePool, rows, old_lens, new_lens, shortfall=None, workspace=None, stream=None):
+    """tq_pages_reserve: rows int32 [n] grow from old_lens to new_lens tokens.  Returns the device
+    int32 [1] shortfall (0 = done)."""
+    n = rows.numel()
+    _same_device(pool.device, rows, old_lens, new_lens, shortfall, workspace)
+    shortfall = _one_int(pool) if shortfall is None else shortfall
+    ws = pool._work(n) if workspace is None else workspace
+    _check(lib().tq_pages_reserve(C.byref(pool.c), _ints(rows, n, "rows"), _ints(old_lens, n, "old_lens"),
+                                  _ints(new_lens, n, "new_lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(),
+                                  ws.numel(), _stream(stream)))
+    return shortfall
+
+
+def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, stream=None):
+    """tq_pages_fork: row dst[i] continues from the first lens[i] tokens of row src[i] (int32 [n]
+    each).  Returns the device int32 [1] shortfall (0 = done)."""
+    n = src.numel()
+    _same_device(pool.device, src, dst, lens, shortfall, workspace)
+    shortfall = _one_int(pool) if shortfall is None else shortfall
+    ws = pool._work(n) if workspace is None else workspace
+    _check(lib().tq_pages_fork(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(src, n, "src"), _ints(dst, n, "dst"),
+                               _ints(lens, n, "lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(), ws.numel(),
+                               _stream(stream)))
+    return shortfall
+
+
+def pages_compact(pool: PagePool, page_map=None, live=None, workspace=None, stream=None):
+    """tq_pages_compact: live pages move to the lowest ids.  Returns page_map int32 [num_pages] (new
+    id of each page, -1: free); live int32 [1], where given, receives their number."""
+    import torch
+    _same_device(pool.device, page_map, live, workspace)
+    page_map = torch.empty(pool.num_pages, dtype=torch.int32, device=pool.device) if page_map is None else page_map
+    live = _one_int(pool) if live is None else live
+    ws = pool._work(0) if workspace is None else workspace
+    _check(lib().tq_pages_compact(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(page_map, pool.num_pages, "page_map"),
+                                  _ints(live, 1, "live"), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return page_map
+
+
+def pages_copy(pool: PagePool, src, dst, stream=None) -> None:
+    """tq_pages_copy: page src[i] to page dst[i] (int32 [n]) in every array of the pool."""
+    n = src.numel()
+    _same_device(pool.device, src, dst)
+    _check(lib().tq_pages_copy(pool.pa, len(pool.arrays), pool.num_pages, _ints(src, n, "src"), _ints(dst, n, "dst"), n,
+                               _stream(stream)))
 
 
 def get_status(stream=None) -> int:
