@@ -92,6 +92,48 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
   return r;
 }
 
+// The line of tiles that a launch cuts into equal runs: virtual sequences v in order, for each its
+// key heads, for each the tiles of its visible tokens.
+struct Kv8Place {
+  int v, h, tile, n;      // virtual sequence, key head, tile and tiles of the sequence
+};
+
+// pref[v]: tiles of one key head before virtual sequence v (pref[VB]: all).
+__device__ __forceinline__ Kv8Place kv8_place_of(int64_t u, const int* pref, int VB, int Hkv) {
+  int lo = 0, hi = VB - 1;
+  while (lo < hi) {                       // last v with Hkv * pref[v] <= u
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(pref[mid]) * Hkv <= u) lo = mid; else hi = mid - 1;
+  }
+  Kv8Place p;
+  p.v = lo;
+  p.n = pref[lo + 1] - pref[lo];
+  const int rem = static_cast<int>(u - static_cast<int64_t>(pref[lo]) * Hkv);
+  p.h = p.n ? rem / p.n : 0;
+  p.tile = p.n ? rem - p.h * p.n : 0;
+  return p;
+}
+
+// Counts pref[1 .. VB] to sums (one warp).
+__device__ __forceinline__ void kv8_prefix(int* pref, int VB) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int v = 0; v < VB; v += 32) {
+    int x = v + lane < VB ? pref[v + lane + 1] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (v + lane < VB) pref[v + lane + 1] = run + x;
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) pref[0] = 0;
+}
+
+// plan[]: tiles a CTA (64 bits), then pref, for the kernel that joins.
+constexpr int kKv8PlanHead = 2;
+
 // The NaN codes (0x7f, 0xff) of four bytes as 0.
 __device__ __forceinline__ uint32_t e4m3_nan_to_zero(uint32_t w) {
   const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;

@@ -135,24 +135,33 @@ tq_status prepare_append(const Append& a, int dtype, int B, int Hkv, int d, cons
 
 // ---- attention
 struct AttnPlan {
-  int64_t VB;          // virtual sequences: groups of 16 rows a sequence
-  int RG, grid;
+  bool prefill;        // the tensor-memory kernel
+  int64_t VB;          // virtual sequences: row groups of a sequence
+  int RG, grid, max_vb;
   size_t off_lse, off_plan, bytes;
 };
 
 size_t up16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-AttnPlan plan_attn(int B, int Hkv, int G, int T, int d, int64_t cap) {
+// 16-bit queries with more than 16 rows a key head take the tensor-memory kernel: it works on 256
+// rows for what the other spends on 16.  fp32 queries always take the other.
+AttnPlan plan_attn(int dtype, int B, int Hkv, int G, int T, int d, int64_t cap) {
   AttnPlan P{};
-  P.RG = static_cast<int>((static_cast<int64_t>(T) * G + kKv8DecodeRows - 1) / kKv8DecodeRows);
+  const int64_t R = static_cast<int64_t>(T) * G;
+  P.prefill = dtype != TQ_F32 && R > kKv8DecodeRows;
+  const int rows = P.prefill ? kKv8PrefillRows : kKv8DecodeRows, tile = P.prefill ? 128 : 32;
+  P.RG = static_cast<int>((R + rows - 1) / rows);
   P.VB = static_cast<int64_t>(B) * P.RG;
+  // the tiles of a launch are counted in 32 bits
+  P.max_vb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(P.prefill ? kKv8PrefillMaxVB : kKv8DecodeMaxVB,
+                                                                     (1ll << 30) / (cap / tile + 2))));
   const int sms = sm_count();
-  // tiles of 32 tokens, eight a CTA at least (one a warp)
-  const int64_t tiles = std::min<int64_t>(P.VB, kKv8DecodeMaxVB) * Hkv * (cap / 32 + 1);
-  P.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (tiles + 7) / 8)));
-  P.off_lse = static_cast<size_t>(2) * sms * kKv8DecodeRows * d * 4;
-  P.off_plan = P.off_lse + up16(static_cast<size_t>(2) * sms * kKv8DecodeRows * 4);
-  P.bytes = P.off_plan + up16((kKv8DecodeMaxVB + 3) * 4);
+  // decode: eight tiles a CTA at least, one a warp
+  const int64_t tiles = std::min<int64_t>(P.VB, P.max_vb) * Hkv * (cap / tile + 2), least = P.prefill ? 1 : 8;
+  P.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (tiles + least - 1) / least)));
+  P.off_lse = static_cast<size_t>(2) * P.grid * rows * d * 4;
+  P.off_plan = P.off_lse + up16(static_cast<size_t>(2) * P.grid * rows * 4);
+  P.bytes = P.off_plan + up16((std::max(kKv8DecodeMaxVB, kKv8PrefillMaxVB) + 3) * 4);
   return P;
 }
 
@@ -179,7 +188,7 @@ tq_status check_attn_shape(int dtype, int B, int Hq, int Hkv, int T, int d) {
   if (s != TQ_OK) return s;
   if (Hq < 1 || Hq % Hkv) return fail(TQ_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
   if (T < 1 || static_cast<int64_t>(T) * (Hq / Hkv) > (1 << 24)) return fail(TQ_ERR_INVALID_ARG, "T out of range");
-  if (static_cast<int64_t>(B) * Hq * T > (1ll << 40)) return fail(TQ_ERR_INVALID_ARG, "too many query rows");
+  if (static_cast<int64_t>(B) * Hq * T > (1ll << 31)) return fail(TQ_ERR_INVALID_ARG, "too many query rows");
   return TQ_OK;
 }
 
@@ -206,7 +215,7 @@ tq_status run_attn(const AttnCall& c) {
   if ((s = strides_of(c.q_strides, c.dtype, c.B, c.Hq, c.T, c.d, qs, q_bytes)) != TQ_OK) return s;
 
   const int G = c.Hq / c.Hkv;
-  const AttnPlan P = plan_attn(c.B, c.Hkv, G, c.T, c.d, m.cap);
+  const AttnPlan P = plan_attn(c.dtype, c.B, c.Hkv, G, c.T, c.d, m.cap);
   if (!c.ws || c.ws_bytes < P.bytes) return fail(TQ_ERR_WORKSPACE, "workspace needs %zu bytes", P.bytes);
   if (!aligned16(c.ws)) return fail(TQ_ERR_ALIGNMENT, "workspace not 16-byte aligned");
 
@@ -237,8 +246,10 @@ tq_status run_attn(const AttnCall& c) {
     if ((s = check_no_alias(outs, 3, fresh, 2)) != TQ_OK || (s = check_no_alias(caches, 4, reads, 5)) != TQ_OK) return s;
   }
   CUtensorMap kmap, vmap;
-  if ((s = byte_rows_map(&kmap, c.kc.codes, recs, c.d, kKv8Block)) != TQ_OK) return s;
-  if ((s = byte_rows_map(&vmap, c.vc.codes, recs, c.d, kKv8Block)) != TQ_OK) return s;
+  if (!P.prefill) {
+    if ((s = byte_rows_map(&kmap, c.kc.codes, recs, c.d, kKv8Block)) != TQ_OK) return s;
+    if ((s = byte_rows_map(&vmap, c.vc.codes, recs, c.d, kKv8Block)) != TQ_OK) return s;
+  }
   cudaError_t e = cudaSuccess;
   if (c.append && (e = launch_kv8_append(ap, c.d, c.stream)) != cudaSuccess) return cuda_fail(e, "append launch");
 
@@ -271,10 +282,11 @@ tq_status run_attn(const AttnCall& c) {
   p.plan = reinterpret_cast<int*>(ws + P.off_plan);
   p.status = device_status_ptr();
   p.wait_limit = wait_limit();
-  for (int64_t v = 0; v < P.VB; v += kKv8DecodeMaxVB) {
+  for (int64_t v = 0; v < P.VB; v += P.max_vb) {
     p.v0 = static_cast<int>(v);
-    p.VB = static_cast<int>(std::min<int64_t>(kKv8DecodeMaxVB, P.VB - v));
-    e = launch_kv8_decode(kmap, vmap, p, c.d, P.grid, c.stream);
+    p.VB = static_cast<int>(std::min<int64_t>(P.max_vb, P.VB - v));
+    e = P.prefill ? launch_kv8_prefill(c.kc.codes, c.vc.codes, p, c.d, P.grid, c.stream)
+                  : launch_kv8_decode(kmap, vmap, p, c.d, P.grid, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
   return TQ_OK;
@@ -385,7 +397,7 @@ tq_status tq_kv8_attn_workspace(int32_t dtype, int32_t B, int32_t Hq, int32_t Hk
   tq_status s = check_attn_shape(dtype, B, Hq, Hkv, T, d);
   if (s != TQ_OK) return s;
   if (!bytes || Nmax < 1 || Nmax > kMaxTokens) return fail(TQ_ERR_INVALID_ARG, "bad workspace query");
-  *bytes = plan_attn(B, Hkv, Hq / Hkv, T, d, Nmax).bytes;
+  *bytes = plan_attn(dtype, B, Hkv, Hq / Hkv, T, d, Nmax).bytes;
   return TQ_OK;
 }
 

@@ -57,9 +57,6 @@ __host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT) {
 }
 static_assert(decode_smem(128, 1).total <= 232448 && decode_smem(128, 2).total <= 232448, "shared memory");
 
-// plan[]: [0] tiles a CTA, [1] virtual sequences, [2 ..] tiles before each (per key head)
-constexpr int kPlanHead = 2;
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -94,26 +91,6 @@ __device__ __forceinline__ float h_lo(float x) { return x - __half2float(__float
 template <int D>
 __device__ __forceinline__ uint32_t swz(int r, uint32_t off) {
   return D == 128 ? r * 128u + (off ^ ((r & 7u) << 4)) : r * 64u + (off ^ (((r >> 1) & 3u) << 4));
-}
-
-// The place of a warp in the line of tiles.
-struct Place {
-  int v, h, tile, n;      // virtual sequence, key head, tile and tiles of the sequence
-};
-
-__device__ __forceinline__ Place place_of(int64_t u, const int* pref, int VB, int Hkv) {
-  int lo = 0, hi = VB - 1;
-  while (lo < hi) {                       // last v with Hkv * pref[v] <= u
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(pref[mid]) * Hkv <= u) lo = mid; else hi = mid - 1;
-  }
-  Place p;
-  p.v = lo;
-  p.n = pref[lo + 1] - pref[lo];
-  const int rem = static_cast<int>(u - static_cast<int64_t>(pref[lo]) * Hkv);
-  p.h = p.n ? rem / p.n : 0;
-  p.tile = p.n ? rem - p.h * p.n : 0;
-  return p;
 }
 
 template <int D, int NT, int W>
@@ -166,34 +143,21 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
   }
   __syncthreads();
-  if (warp == 0) {                         // prefix sums, 32 at a time
-    int run = 0;
-    for (int v = 0; v < VB; v += 32) {
-      int x = v + lane < VB ? s_pref[v + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (v + lane < VB) s_pref[v + lane + 1] = run + x;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) s_pref[0] = 0;
-  }
+  if (warp == 0) kv8_prefix(s_pref, VB);
   __syncthreads();
   const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
   const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinTiles));
   if (blockIdx.x == 0) {
-    for (int v = tid; v <= VB; v += kWarps * 32) p.plan[kPlanHead + v] = s_pref[v];
-    if (tid == 0) { p.plan[0] = static_cast<int>(per); p.plan[1] = VB; }
+    for (int v = tid; v <= VB; v += kWarps * 32) p.plan[kKv8PlanHead + v] = s_pref[v];
+    if (tid == 0) *reinterpret_cast<int64_t*>(p.plan) = per;
   }
   pdl_trigger();
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
 
   // ---- issue side: this warp's tiles u0 + warp, + kWarps, ...
   int64_t iu = u0 + warp;
-  Place ip{};
-  if (iu < u1) ip = place_of(iu, s_pref, VB, Hkv);
+  Kv8Place ip{};
+  if (iu < u1) ip = kv8_place_of(iu, s_pref, VB, Hkv);
   int issued = 0, used = 0;
   auto issue = [&]() {
     if (iu >= u1) return;
@@ -236,7 +200,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   int64_t cu = u0 + warp;
   bool dead = false;
   for (int64_t u = u0; u < u1;) {
-    const Place sp = place_of(u, s_pref, VB, Hkv);
+    const Kv8Place sp = kv8_place_of(u, s_pref, VB, Hkv);
     const int64_t seg_end = min(u1, u + sp.n - sp.tile);
     const int gv = p.v0 + sp.v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
     const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, nullptr);
@@ -552,13 +516,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     if (warp == 0) {
       const bool whole = sp.tile == 0 && seg_end - u == sp.n;
-      const float unit = ex2(Em - (127.f + 15.f));      // of the accumulated values
+      // the sums are in units of 2^(Em - 127 - 15); two factors, so that neither leaves the normal range
+      const float unit = __uint_as_float(static_cast<uint32_t>(Em) << 23);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int rl = nt * 8 + 2 * qd + c, r = r0 + rl;
-          const float inv = Ls[nt][c] == 0.f ? 0.f : unit / Ls[nt][c];
+          const float inv = Ls[nt][c] == 0.f ? 0.f : 1.f / (Ls[nt][c] * 32768.f);
           const float ls2 = Ls[nt][c] == 0.f ? -INFINITY : M[nt][c] + __log2f(Ls[nt][c]);
           if (whole) {
             if (r < R) {
@@ -567,7 +532,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
               if (p.lse && g == 0) p.lse[row] = ls2 * kLn2;
 #pragma unroll
               for (int k = 0; k < MT; ++k) {
-                const float x = acc[k][nt][c] * inv, y = acc[k][nt][2 + c] * inv;
+                const float x = acc[k][nt][c] * inv * unit, y = acc[k][nt][2 + c] * inv * unit;
                 const int64_t at = row * D + (D / 8) * g + 2 * k;
                 if (W == 2) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
                 else if (p.dtype == TQ_BF16)
@@ -581,7 +546,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             float* o = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + (D / 8) * g;
 #pragma unroll
             for (int k = 0; k < MT; ++k)
-              *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][nt][c] * inv, acc[k][nt][2 + c] * inv);
+              *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][nt][c] * inv * unit, acc[k][nt][2 + c] * inv * unit);
           }
         }
     }
@@ -600,8 +565,8 @@ __global__ void __launch_bounds__(128) kv8_decode_join_kernel(const Kv8AttnParam
   pdl_wait();
   pdl_trigger();
   const int Hkv = p.map.Hkv, v = blockIdx.x / Hkv, h = blockIdx.x - v * Hkv;
-  const int64_t per = __ldg(p.plan);
-  const int t0 = __ldg(p.plan + kPlanHead + v), n = __ldg(p.plan + kPlanHead + v + 1) - t0;
+  const int64_t per = __ldg(reinterpret_cast<const int64_t*>(p.plan));
+  const int t0 = __ldg(p.plan + kKv8PlanHead + v), n = __ldg(p.plan + kKv8PlanHead + v + 1) - t0;
   const int64_t u = static_cast<int64_t>(t0) * Hkv + static_cast<int64_t>(h) * n;
   const int c0 = static_cast<int>(u / per), c1 = n ? static_cast<int>((u + n - 1) / per) : c0;
   if (n && c0 == c1) return;                   // finished where it was computed

@@ -48,4 +48,11 @@ constexpr int kKv8DecodeMaxVB = 1024;                 // virtual sequences a lau
 cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
                               cudaStream_t s);
 
+
+// Groups of 256 rows a key head, 16-bit queries (prefill).
+constexpr int kKv8PrefillRows = 256;
+constexpr int kKv8PrefillMaxVB = 1024;
+cudaError_t launch_kv8_prefill(const uint8_t* kcodes, const uint8_t* vcodes, const Kv8AttnParams& p, int d, int grid,
+                               cudaStream_t s);
+
 }  // namespace tq
