@@ -131,6 +131,25 @@ __device__ __forceinline__ void kv8_prefix(int* pref, int VB) {
   if (lane == 0) pref[0] = 0;
 }
 
+// A CTA that starts inside a key head's units says so for the kernel that joins: plan[c] = {v, h, c0,
+// c1}, the CTAs that worked on it, if c is the second of them, else v = -1.  A key head has COST
+// units before its tiles.
+template <int COST>
+__device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1, int64_t per, const int* pref, int VB, int Hkv) {
+  int4 s = make_int4(-1, 0, 0, 0);
+  if (u0 < u1 && u0 > 0) {
+    const Kv8Place p = kv8_place_of(u0, pref, VB, Hkv);
+    const int64_t start = u0 - p.tile;
+    s.z = static_cast<int>((start + COST) / per);
+    s.w = static_cast<int>((start + p.n - 1) / per);
+    if (p.tile > 0 && s.z + 1 == static_cast<int>(blockIdx.x)) {
+      s.x = p.v;
+      s.y = p.h;
+    }
+  }
+  reinterpret_cast<int4*>(plan)[blockIdx.x] = s;
+}
+
 // plan[]: tiles a CTA (64 bits), then pref, for the kernel that joins.
 constexpr int kKv8PlanHead = 2;
 

@@ -51,7 +51,7 @@ cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, 
 
 // Groups of 256 rows a key head, 16-bit queries (prefill).
 constexpr int kKv8PrefillRows = 256;
-constexpr int kKv8PrefillMaxVB = 1024;
+constexpr int kKv8PrefillMaxVB = 512;
 cudaError_t launch_kv8_prefill(const uint8_t* kcodes, const uint8_t* vcodes, const Kv8AttnParams& p, int d, int grid,
                                cudaStream_t s);
 

@@ -31,17 +31,40 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kTile = 128;                   // tokens, and rows of a row tile
 constexpr int kBlocks = kTile / kKv8Block;
 constexpr float kLazy = 8.f;                 // a reference may lag by this many powers of two
 constexpr int kHead = 7;                     // P <= 2^(kLazy + kHead)
 constexpr int kScaleSlots = 4;               // tiles whose scales are kept: a slot is filled again when the
                                              // first product of the tile two before is done, so none in use
-constexpr int kSlot = 2 * kBlocks + 4;       // key scales, exponents of the probabilities, E
+constexpr int kSlot = 3 * kBlocks + 4;       // key scales, exponents f of the probabilities, 2^-f, E
+constexpr int kRunCost = 2;                  // what a run costs beside its tiles, in tiles
+// Registers a thread of the roles' warpgroups; the launch has 128 for each of 512 threads.
+constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsRest = 56, kRegsLaunch = 128;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
+constexpr int kScouts = 96;                  // threads of the three warps that prepare runs
+
+// A run: tiles [tile, tile + tiles) of the n of key head h of virtual sequence v, which is rows r0 ..
+// of sequence b; tile 0 of the run starts at token t0.  tiles = 0: no more.
+struct Run {
+  int v, h, tile, tiles, n, units, b, r0, t0;
+  int lo, hi;                                // tokens that some row sees
+  int in_lo, in_hi;                          // tokens that all rows see
+};
+
+struct RowMeta {                             // of 256 rows
+  Run run;
+  int lo[kKv8PrefillRows], hi[kKv8PrefillRows], pos[kKv8PrefillRows];
+  float slope[kKv8PrefillRows];
+  int i[kKv8PrefillRows], hq[kKv8PrefillRows];       // query and head; i = -1: no row
+};
+
+// Blocks of codes on their way, for each converting warp.
+__host__ __device__ constexpr int raw_slots(int D) { return D == 64 ? 4 : 2; }
 
 struct PrefillSmem {
-  uint32_t q, k, v, scales, bars, lo, hi, in_lo, in_hi, pref, misc, total;
+  uint32_t q, k, v, raw, meta, scales, bars, pref, misc, total;
 };
 __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   PrefillSmem L{};
@@ -50,12 +73,10 @@ __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   L.q = at; at += 2 * tile;
   L.k = at; at += 2 * tile;
   L.v = at; at += 2 * tile;
+  L.raw = at; at += 4 * raw_slots(D) * kKv8Block * D;
+  L.meta = at; at += 2 * sizeof(RowMeta);
   L.scales = at; at += kScaleSlots * kSlot * 4;
-  L.bars = at; at += 16 * 8;
-  L.lo = at; at += kKv8PrefillMaxVB * 4;
-  L.hi = at; at += kKv8PrefillMaxVB * 4;
-  L.in_lo = at; at += kKv8PrefillMaxVB * 4;
-  L.in_hi = at; at += kKv8PrefillMaxVB * 4;
+  L.bars = at; at += 38 * 8;
   L.pref = at; at += (kKv8PrefillMaxVB + 4) * 4;
   L.misc = at; at += 64;
   L.total = at + 1024;
@@ -63,7 +84,7 @@ __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
 }
 static_assert(prefill_smem(128).total <= 232448, "shared memory");
 
-enum : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, OFULL = 12, QFULL = 14 };
+enum : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, OFULL = 12, QFULL = 14, MEMPTY = 16, DFULL = 18, PHALF = 20, RAW = 22 /* + 4 warp + slot */ };
 
 // Operand tile of 128 rows of D halves: D / 64 parts of [128][64], 16-byte chunks XORed with the
 // row within 8.  Byte offset of chunk c (8 halves) of row r.
@@ -92,14 +113,87 @@ __device__ __forceinline__ uint32_t idesc_f16(uint32_t n, uint32_t tb) {
   return (1u << 4) | (tb << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t a, const float (&v)[32]) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// 16 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
   uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// No use of v before this point (the wait for its load from tensor memory).
+__device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
-    tmem_st16(a + 16 * h, r);
-  }
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+f"(v[k]));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
+  return on != 0;
+}
+
+// Two floats an instruction.
+__device__ __forceinline__ float2 pair(float x, float y) { return make_float2(x, y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+
+// tanh for |z| <= 1/2: the series to z^11, whose next term is below 2^-21.
+__device__ __forceinline__ float2 tanh_small(float2 z) {
+  const float2 u = mul2(z, z);
+  float2 p = fma2(u, both(-1382.f / 155925.f), both(62.f / 2835.f));
+  p = fma2(u, p, both(-17.f / 315.f));
+  p = fma2(u, p, both(2.f / 15.f));
+  p = fma2(u, p, both(-1.f / 3.f));
+  return fma2(mul2(z, u), p, z);
+}
+
+// The run that starts at unit u of the line and ends at u1 or with its key head.  A key head takes
+// kRunCost units and one for each tile.
+__device__ __forceinline__ Run run_at(int64_t u, int64_t u1, const int* pref, int VB, int Hkv) {
+  const Kv8Place p = kv8_place_of(u, pref, VB, Hkv);
+  Run r;
+  r.v = p.v;
+  r.h = p.h;
+  r.n = p.n - kRunCost;
+  r.units = static_cast<int>(min(u1 - u, static_cast<int64_t>(p.n - p.tile)));
+  r.tile = max(0, p.tile - kRunCost);
+  r.tiles = max(0, p.tile + r.units - kRunCost) - r.tile;
+  r.b = r.r0 = r.t0 = r.lo = r.hi = r.in_lo = r.in_hi = 0;
+  return r;
 }
 
 // GEN: scores are capped or biased.
@@ -112,15 +206,11 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   const uint32_t raw = smem_u32(psm_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* sm = psm_raw + (base - raw);
+  RowMeta* s_meta = reinterpret_cast<RowMeta*>(sm + L.meta);
   float* s_scale = reinterpret_cast<float*>(sm + L.scales);
-  int* s_lo = reinterpret_cast<int*>(sm + L.lo);                // tokens that some row of the group sees
-  int* s_hi = reinterpret_cast<int*>(sm + L.hi);
-  int* s_in_lo = reinterpret_cast<int*>(sm + L.in_lo);          // tokens that all rows see
-  int* s_in_hi = reinterpret_cast<int*>(sm + L.in_hi);
   int* s_pref = reinterpret_cast<int*>(sm + L.pref);
-  int* s_e = reinterpret_cast<int*>(sm + L.misc);               // [4] largest value scale that each converting warp saw
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L.misc + 32);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc + 36);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L.misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc + 4);
   const uint32_t bar0 = base + L.bars;
   auto bar = [&](int id) { return bar0 + 8u * id; };
 
@@ -135,7 +225,11 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       mbar_init(bar(PFULL + i), 128);
       mbar_init(bar(OFULL + i), 1);
       mbar_init(bar(QFULL + i), 128);
+      mbar_init(bar(MEMPTY + i), 256 + 4 + 1);         // softmax threads, converting and issuing warps
+      mbar_init(bar(PHALF + i), 128);
+      mbar_init(bar(DFULL + i), kScouts);
     }
+    for (int i = 0; i < 16; ++i) mbar_init(bar(RAW + i), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -148,10 +242,9 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
 
   // ---- how the work is cut
   const int VB = p.VB, Hkv = p.map.Hkv, R = p.T * p.G;
-  for (int v = warp; v < VB; v += kThreads / 32) {
-    const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8PrefillRows;
-    const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, p.status);
-    int lo = INT32_MAX, hi = 0, in_lo = 0, in_hi = INT32_MAX;
+  // Tokens that some row, and that all rows, of a group see (one warp).
+  auto group_range = [&](int b, int r0, int len, int& lo, int& hi, int& in_lo, int& in_hi) {
+    lo = INT32_MAX, hi = 0, in_lo = 0, in_hi = INT32_MAX;
     const int i1 = min(R - 1, r0 + kKv8PrefillRows - 1) / p.G;
     for (int i = r0 / p.G + lane; i <= i1; i += 32) {
       int a, z, pos;
@@ -164,13 +257,13 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     hi = __reduce_max_sync(0xffffffffu, hi);
     in_lo = __reduce_max_sync(0xffffffffu, in_lo);
     in_hi = __reduce_min_sync(0xffffffffu, in_hi);
-    if (lane == 0) {
-      s_lo[v] = hi > 0 ? lo : 0;
-      s_hi[v] = hi;
-      s_in_lo[v] = in_lo;
-      s_in_hi[v] = in_hi;
-      s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
-    }
+  };
+  for (int v = warp; v < VB; v += kThreads / 32) {
+    const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8PrefillRows;
+    const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, p.status);
+    int lo, hi, in_lo, in_hi;
+    group_range(b, r0, len, lo, hi, in_lo, in_hi);
+    if (lane == 0) s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile + kRunCost : 0;
   }
   __syncthreads();
   if (warp == 0) kv8_prefix(s_pref, VB);
@@ -180,380 +273,570 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   const uint32_t tmem = *tmem_slot;
   const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
   const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
-  if (blockIdx.x == 0) {
-    for (int v = tid; v <= VB; v += kThreads) p.plan[kKv8PlanHead + v] = s_pref[v];
-    if (tid == 0) *reinterpret_cast<int64_t*>(p.plan) = per;
-  }
-  pdl_trigger();
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
+  if (tid == 0) kv8_plan_split<kRunCost>(p.plan, u0, u1, per, s_pref, VB, Hkv);
+  pdl_trigger();
   const long long lim = p.wait_limit;
 
   if (warp < 8) {
     // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int rt = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + rt * 128, to = tmem + lanes + 256 + rt * D;
+    int kt = 0, own = 0, oseg = 0;           // tiles of the CTA, tiles and runs of this row tile
+    const bool bf = p.dtype == TQ_BF16;
+    const int rr = rt * kTile + row;
     const uint32_t qa = base + L.q + rt * TB;
-    int64_t kt = 0;                          // tiles of the CTA so far
-    int own = 0, seg = 0;                    // tiles and runs of this row tile
+    float rowc = 0.f;
+    uint4 qx[D / 8];                         // the next run's row of q, on its way
+    bool loaded = false;                     // the run was waited for, its q asked for
+    auto load_q = [&](const RowMeta& meta, bool want) {
+      const int i = want ? meta.i[rr] : -1;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(p.q) + meta.run.b * p.q_stride_b + meta.hq[rr] * p.q_stride_h + i * p.q_stride_t);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) qx[c] = i >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    };
+    // The row divided by a power of two, its largest entry in [1, 2), as an operand.
+    auto store_q = [&]() {
+      auto unpack = [&](uint32_t w) {
+        return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                  : __half22float2(*reinterpret_cast<const __half2*>(&w));
+      };
+      float mx = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w[4] = {qx[c].x, qx[c].y, qx[c].z, qx[c].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack(w[k]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 1), 253);
+      float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      rowc = __uint_as_float(static_cast<uint32_t>(e) << 23) * fabsf(p.sc.scale_log2);
+      if (p.sc.scale_log2 < 0.f) down = -down;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w[4] = {qx[c].x, qx[c].y, qx[c].z, qx[c].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack(w[k]);
+          y[k] = pack_h2(f.x * down, f.y * down);
+        }
+        sts128(qa + tile_off(row, c), y[0], y[1], y[2], y[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(bar(QFULL + rt));
+    };
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok;) {
-      const Kv8Place sp = kv8_place_of(u, s_pref, VB, Hkv);
-      const int64_t seg_end = min(u1, u + sp.n - sp.tile);
-      const int tiles = static_cast<int>(seg_end - u);
-      const int gv = p.v0 + sp.v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8PrefillRows;
-      if (r0 + rt * kTile >= R) {            // this row tile is empty
+    for (int seg = 0;; ++seg) {
+      const RowMeta& meta = s_meta[seg & 1];
+      const Run& run = meta.run;
+      if (!loaded) ok = __all_sync(0xffffffffu, mbar_wait(bar(DFULL + (seg & 1)), (seg >> 1) & 1, lim, p.status, abort_flag));
+      const int tiles = run.tiles;
+      if (!ok || tiles == 0) break;
+      if (run.r0 + rt * kTile >= R) {        // this row tile is empty
         kt += tiles;
-        u = seg_end;
+        loaded = false;
+        mbar_arrive(bar(MEMPTY + (seg & 1)));
         continue;
       }
-      const int r = r0 + rt * kTile + row;
-      const bool on = r < R;
-      const int i = on ? r / p.G : 0, hq = sp.h * p.G + (on ? r - i * p.G : 0);
-      const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, nullptr);
-      int lo = 0, hi = 0, pos = 0;
-      float slope = 0.f;
-      if (on) {
-        kv8_range(p.sc, b, i, p.T, len, lo, hi, pos);
-        if (GEN && p.sc.slopes) slope = __ldg(p.sc.slopes + hq) * kLog2E;
-      }
-      // ---- the row of q, divided by a power of two
-      float rowc;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + b * p.q_stride_b + hq * p.q_stride_h + i * p.q_stride_t);
-        const bool bf = p.dtype == TQ_BF16;
-        auto unpack = [&](uint32_t w) {
-          return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
-                    : __half22float2(*reinterpret_cast<const __half2*>(&w));
-        };
-        uint4 x[D / 8];
-        float mx = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          x[c] = on ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack(w[k]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-        const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23), 1), 253);
-        float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        rowc = __uint_as_float(static_cast<uint32_t>(e) << 23) * fabsf(p.sc.scale_log2);
-        if (p.sc.scale_log2 < 0.f) down = -down;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack(w[k]);
-            y[k] = pack_h2(f.x * down, f.y * down);
-          }
-          sts128(qa + tile_off(row, c), y[0], y[1], y[2], y[3]);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(bar(QFULL + rt));
-      }
-      // tokens that all rows of this warp see
-      const int w_lo = __reduce_max_sync(0xffffffffu, on ? lo : 0);
-      const int w_hi = __reduce_min_sync(0xffffffffu, on ? hi : INT32_MAX);
-      const int tile0 = s_lo[sp.v] / kTile + sp.tile;
-
+      if (!loaded) load_q(meta, true);
+      store_q();
+      loaded = false;
+      int t0 = run.t0;
+      const int lo = meta.lo[rr], hi = meta.hi[rr], pos = GEN ? meta.pos[rr] : 0;
+      const float slope = GEN ? meta.slope[rr] : 0.f;
       float m = -INFINITY, l = 0.f, E = 1.f;
-      for (int j = 0; j < tiles; ++j, ++kt, ++own) {
+      for (int j = 0; j < tiles; ++j, ++kt, ++own, t0 += kTile) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + rt), own & 1, lim, p.status, abort_flag));
         if (!ok) break;
         tc_fence_after();
+        // the row's scores stay in registers (the probabilities overwrite them in tensor memory)
+        float s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(ts, s0);
+        tmem_ld32(ts + 32, s1);
         const float* sc = s_scale + (kt % kScaleSlots) * kSlot;
-        E = sc[2 * kBlocks];
-        const int t0 = (tile0 + j) * kTile;
-        const bool masked = t0 < w_lo || t0 + kTile > w_hi;
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < kTile / 32; ++c) {
-          float s[32];
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld();
-          const float c0 = sc[2 * c] * rowc, c1 = sc[2 * c + 1] * rowc;
-          if (GEN || masked) {
+        const float E1 = sc[3 * kBlocks];
+        const bool masked = __any_sync(0xffffffffu, t0 < lo || t0 + kTile > hi);
+        const bool formed = GEN || masked;   // scores are formed here, else their scale joins the exponent
+        // Forms the scores of 32 tokens (their quarter: c), and their maximum.
+        auto top = [&](float (&s)[32], int c) {
+          if (formed) {
+            if (GEN && p.sc.cap > 0.f) {
+              const float by_cap = kLn2 / p.sc.cap * rowc, cap2 = p.sc.cap * kLog2E;
+              const float z0 = sc[2 * c] * by_cap, z1 = sc[2 * c + 1] * by_cap;
+              float far = 0.f, far1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int t = t0 + 32 * c + k;
-              float x = s[k] * (k < 16 ? c0 : c1);
-              if (GEN) {
-                if (p.sc.cap > 0.f) x = p.sc.cap * kLog2E * kv8_tanh(x * (kLn2 / p.sc.cap));
-                if (p.sc.slopes) x -= slope * static_cast<float>(abs(pos - t));
+              for (int k = 0; k < 16; ++k) {
+                far = fmaxf(far, fabsf(s[k]));
+                far1 = fmaxf(far1, fabsf(s[16 + k]));
               }
-              if (masked && (t < lo || t >= hi)) x = -INFINITY;
-              s[k] = x;
-              mx = fmaxf(mx, x);
-            }
-            tmem_st32(ts + 32 * c, s);
-          } else {
-            float a = s[0], d = s[16];
+              if (__all_sync(0xffffffffu, fmaxf(far * z0, far1 * z1) <= 0.5f)) {
 #pragma unroll
-            for (int k = 1; k < 16; ++k) { a = fmaxf(a, s[k]); d = fmaxf(d, s[16 + k]); }
-            mx = fmaxf(mx, fmaxf(a * c0, d * c1));
+                for (int k = 0; k < 32; k += 2) {
+                  const float2 y = mul2(tanh_small(mul2(pair(s[k], s[k + 1]), both(k < 16 ? z0 : z1))), both(cap2));
+                  s[k] = y.x;
+                  s[k + 1] = y.y;
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = cap2 * kv8_tanh(s[k] * (k < 16 ? z0 : z1));
+              }
+            } else {
+              const float z0 = sc[2 * c] * rowc, z1 = sc[2 * c + 1] * rowc;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] *= k < 16 ? z0 : z1;
+            }
+            if (GEN && p.sc.slopes) {
+              const float far0 = static_cast<float>(pos - t0 - 32 * c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[k] = fmaf(-slope, fabsf(far0 - k), s[k]);
+            }
+            if (masked) {
+              const int a = lo - t0 - 32 * c, z = hi - t0 - 32 * c;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k < a || k >= z) s[k] = -INFINITY;
+            }
           }
-        }
-        if (GEN || masked) tmem_wait_st();
-        // ---- the reference, and what was summed against the old one
+          float a = s[0], b = s[16];
+#pragma unroll
+          for (int k = 1; k < 16; ++k) {
+            a = fmaxf(a, s[k]);
+            b = fmaxf(b, s[16 + k]);
+          }
+          return formed ? fmaxf(a, b) : fmaxf(a * (sc[2 * c] * rowc), b * (sc[2 * c + 1] * rowc));
+        };
+        tmem_wait_ld();
+        pin(s0);
+        pin(s1);
+        tmem_ld32(ts + 64, s2);
+        tmem_ld32(ts + 96, s3);
+        float mx = fmaxf(top(s0, 0), top(s1, 1));
+        tmem_wait_ld();
+        pin(s2);
+        pin(s3);
+        mx = fmaxf(mx, fmaxf(top(s2, 2), top(s3, 3)));
+        // ---- the reference, and what was summed against the old one and the old E
         const bool grow = mx > m + kLazy || m == -INFINITY;
         const float m1 = grow ? fmaxf(m, mx) : m;
         const float ref = m1 == -INFINITY ? 0.f : m1;
-        if (j > 0 && __any_sync(0xffffffffu, grow && mx > m)) {
+        if (j > 0 && __any_sync(0xffffffffu, (grow && mx > m) || E1 != E)) {
           const float a = ex2(m - ref);      // 1 where the reference stays, 0 where there was none
           l *= a;
+          const float ae = a * ex2(E - E1);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32(to + 32 * c, o);
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tmem_ld16(to + 16 * c, o);
             tmem_wait_ld();
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= a;
-            tmem_st32(to + 32 * c, o);
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * ae);
+            tmem_st16(to + 16 * c, w);
           }
         }
         m = m1;
+        E = E1;
         // ---- probabilities
-#pragma unroll 1
-        for (int c = 0; c < kTile / 32; ++c) {
-          float s[32];
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld();
-          uint32_t out[16];
+        // The exponentials of 32 tokens stand between the sums and the rounding of the 32 before, so
+        // that their unit, which bounds this part, is not left waiting.
+        auto arg = [&](float (&s)[32], int c) {
+          const float2 off0 = both(sc[kBlocks + 2 * c] - ref), off1 = both(sc[kBlocks + 2 * c + 1] - ref);
+          const float2 cb0 = both(formed ? 1.f : sc[2 * c] * rowc), cb1 = both(formed ? 1.f : sc[2 * c + 1] * rowc);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = sc[kBlocks + 2 * c + h];
-            const float cc = (GEN || masked) ? 1.f : sc[2 * c + h] * rowc;
-            const float off = f - ref;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float x = ex2(fmaf(s[16 * h + k], cc, off)), y = ex2(fmaf(s[16 * h + k + 1], cc, off));
-              sum += x + y;
-              out[8 * h + k / 2] = pack_h2(x, y);
-            }
-            l = fmaf(sum, ex2(-f), l);
+          for (int k = 0; k < 32; k += 2) {
+            const float2 x = fma2(pair(s[k], s[k + 1]), k < 16 ? cb0 : cb1, k < 16 ? off0 : off1);
+            s[k] = x.x;
+            s[k + 1] = x.y;
           }
-          tmem_st16(ts + 16 * c, out);
+        };
+        auto ex2_at = [](float& x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); };
+        uint32_t out[16];
+        float2 sum;
+        auto finish_at = [&](const float (&s)[32], int c, int k) {         // the pair k of 16
+          const float2 x = pair(s[2 * k], s[2 * k + 1]);
+          asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(out[k]) : "f"(x.y), "f"(x.x));
+          sum = (k & 7) ? add2(sum, x) : x;
+          if ((k & 7) == 7) l = fmaf(sum.x + sum.y, sc[2 * kBlocks + 2 * c + (k >> 3)], l);
+        };
+        arg(s0, 0);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) ex2_at(s0[k]);
+        arg(s1, 1);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          ex2_at(s1[k]);
+          if (k & 1) finish_at(s0, 0, k >> 1);
         }
+        tmem_st16(ts, out);
+        arg(s2, 2);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          ex2_at(s2[k]);
+          if (k & 1) finish_at(s1, 1, k >> 1);
+        }
+        tmem_st16(ts + 16, out);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(PHALF + rt));        // the second product may begin
+        arg(s3, 3);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          ex2_at(s3[k]);
+          if (k & 1) finish_at(s2, 2, k >> 1);
+        }
+        tmem_st16(ts + 32, out);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) finish_at(s3, 3, k);
+        tmem_st16(ts + 48, out);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(PFULL + rt));
       }
       if (!ok) break;
-      // ---- the run's result
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(OFULL + rt), seg & 1, lim, p.status, abort_flag));
+      // ---- the next run's row of q is asked for before this run's result is waited for
+      const RowMeta& after = s_meta[(seg & 1) ^ 1];
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(DFULL + ((seg + 1) & 1)), ((seg + 1) >> 1) & 1, lim, p.status, abort_flag));
       if (!ok) break;
+      loaded = true;
+      load_q(after, after.run.tiles > 0 && after.run.r0 + rt * kTile < R);
+      // ---- the run's result
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(OFULL + rt), oseg & 1, lim, p.status, abort_flag));
+      if (!ok) break;
+      ++oseg;
       tc_fence_after();
-      const bool whole = sp.tile == 0 && tiles == sp.n;
+      const bool whole = tiles == run.n;
       // O is in units of 2^(E - 127 - kHead); two factors, so that neither leaves the normal range
       const float unit = __uint_as_float(static_cast<uint32_t>(E) << 23);
       const float inv = l == 0.f ? 0.f : 1.f / (l * (1 << kHead));
       const float ls2 = l == 0.f ? -INFINITY : m + __log2f(l);
-      const int64_t at = (static_cast<int64_t>(b) * p.Hq + hq) * p.T + i;
-      const int slot = blockIdx.x * 2 + (sp.tile == 0 ? 1 : 0);
-      const int64_t prow = static_cast<int64_t>(slot) * kKv8PrefillRows + rt * kTile + row;
+      const bool on = meta.i[rr] >= 0;
+      const int64_t at = (static_cast<int64_t>(run.b) * p.Hq + meta.hq[rr]) * p.T + meta.i[rr];
+      const int slot = blockIdx.x * 2 + (run.tile == 0 ? 1 : 0);
+      mbar_arrive(bar(MEMPTY + (seg & 1)));  // (behind the last use of run and meta)
+      const int64_t prow = static_cast<int64_t>(slot) * kKv8PrefillRows + rr;
       if (on) {
         if (whole) { if (p.lse) p.lse[at] = ls2 * kLn2; }
         else p.part_lse[prow] = ls2;
       }
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32(to + 32 * c, o);
+      for (int c = 0; c < D / 16; ++c) {
+        float o[16];
+        tmem_ld16(to + 16 * c, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = o[k] * inv * unit;
+        for (int k = 0; k < 16; ++k) o[k] = o[k] * inv * unit;
         if (on && whole) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (p.dtype == TQ_BF16) {
+          for (int k = 0; k < 8; ++k) {
+            if (bf) {
               const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
               w[k] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
               w[k] = pack_h2(o[2 * k], o[2 * k + 1]);
             }
           }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 32 * c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 16 * c);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else if (on) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 16 * c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 4; ++k)
             dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
         __syncwarp();
       }
       tc_fence_before();                     // before the next run's products overwrite O
-      ++seg;
-      u = seg_end;
+    }
+    // ---- groups that see nothing
+    for (int v = blockIdx.x; v < VB; v += gridDim.x) {
+      if (s_pref[v + 1] != s_pref[v]) continue;
+      const int gv = p.v0 + v, b = gv / p.RG, r = (gv - b * p.RG) * kKv8PrefillRows + tid;
+      if (r >= R) continue;
+      const int i = r / p.G, g = r - i * p.G;
+      for (int h = 0; h < Hkv; ++h) {
+        const int64_t at = (static_cast<int64_t>(b) * p.Hq + h * p.G + g) * p.T + i;
+        if (p.lse) p.lse[at] = -INFINITY;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D);
+        for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(0, 0, 0, 0);
+      }
     }
   } else if (warp < 12) {
     // ================================================================ codes to halves
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    // Warp w takes blocks w and w + 4 of each tile's keys, then of its values; its blocks of codes
+    // arrive in a ring of its own.
     const int w = warp - 8;
-    int64_t kt = 0;
-    bool ok = true;                          // a thread that gave up still takes part in the barriers
-    constexpr int NL = D / 16;               // 16-byte loads a thread and tile: rows 8 (w + 4 k) + lane % 8
-    constexpr int NH = D / 64;
-    for (int64_t u = u0; u < u1;) {
-      const Kv8Place sp = kv8_place_of(u, s_pref, VB, Hkv);
-      const int64_t seg_end = min(u1, u + sp.n - sp.tile);
-      const int tiles = static_cast<int>(seg_end - u);
-      const int b = (p.v0 + sp.v) / p.RG;
-      const int b_lo = s_lo[sp.v] / kKv8Block, b_hi = (s_hi[sp.v] - 1) / kKv8Block;
-      const int tile0 = s_lo[sp.v] / kTile + sp.tile;
-      // record of a block; one outside the visible tokens may have no page: the nearest visible
-      auto block_rec = [&](int blk) {
-        return kv8_record(p.map, b, sp.h, static_cast<int64_t>(min(max(blk, b_lo), b_hi)) * kKv8Block, p.status);
-      };
-      // largest value scale of the run
-      int E = 1;
-      for (int blk = max(tile0 * kBlocks, b_lo) + w * 32 + lane; blk <= min((tile0 + tiles) * kBlocks - 1, b_hi); blk += 128)
-        E = max(E, static_cast<int>((__float_as_uint(__ldg(p.vscales + block_rec(blk) / kKv8Block)) >> 23) & 0xffu));
-      E = __reduce_max_sync(0xffffffffu, E);
-      if (lane == 0) s_e[w] = E;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      E = max(max(s_e[0], s_e[1]), max(s_e[2], s_e[3]));
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-
-      // row 8 (w + 4 k) + lane % 8 of a tile lies in block (w + 4 k) / 2
-      uint4 raw_k[NL], raw_v[NL];
-      float next_scale = 0.f;
-      auto load = [&](const uint8_t* codes, int tile, uint4 (&x)[NL]) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = 8 * (w + 4 * k) + (lane & 7);
-          const int64_t rec = block_rec(tile * kBlocks + rr / kKv8Block) + rr % kKv8Block;
-#pragma unroll
-          for (int h = 0; h < NH; ++h)
-            x[k * NH + h] = __ldg(reinterpret_cast<const uint4*>(codes + rec * D + h * 64 + (lane >> 3) * 16));
-        }
-      };
-      auto load_scales = [&](int tile) {     // threads 0..7 key scales, 8..15 value scales
-        if (w == 0 && lane < 2 * kBlocks)
-          next_scale = __ldg((lane < kBlocks ? p.kscales : p.vscales) + block_rec(tile * kBlocks + lane % kBlocks) / kKv8Block);
-      };
-      auto convert = [&](uint4 (&x)[NL], uint32_t dst, bool clean) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = 8 * (w + 4 * k) + (lane & 7);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint4 y = x[k * NH + h];
-            if (clean) {
-              y.x = e4m3_nan_to_zero(y.x);
-              y.y = e4m3_nan_to_zero(y.y);
-              y.z = e4m3_nan_to_zero(y.z);
-              y.w = e4m3_nan_to_zero(y.w);
-            }
-            const int c = h * 8 + (lane >> 3) * 2;
-            sts128(dst + tile_off(rr, c), e4m3x2_to_h2(y.x), e4m3x2_to_h2(y.x >> 16), e4m3x2_to_h2(y.y),
-                   e4m3x2_to_h2(y.y >> 16));
-            sts128(dst + tile_off(rr, c + 1), e4m3x2_to_h2(y.z), e4m3x2_to_h2(y.z >> 16), e4m3x2_to_h2(y.w),
-                   e4m3x2_to_h2(y.w >> 16));
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      };
-      if (ok) {
-        load_scales(tile0);
-        load(kcodes, tile0, raw_k);
-      }
-      for (int j = 0; j < tiles && ok; ++j, ++kt) {
-        const int st = static_cast<int>(kt & 1);
-        const uint32_t ph = static_cast<uint32_t>((kt >> 1) - 1) & 1u;
-        const int t0 = (tile0 + j) * kTile;
-        load(vcodes, tile0 + j, raw_v);
-        if (kt >= 2 && !mbar_wait(bar(KEMPTY + st), ph, lim, p.status, abort_flag)) { ok = false; break; }
-        if (w == 0 && lane <= 2 * kBlocks) {
-          float x = next_scale;
-          if (lane == 2 * kBlocks) x = static_cast<float>(E);
-          else if (lane >= kBlocks)          // exponent of the block's probabilities
-            x = static_cast<float>(kHead + max(static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - E, -100));
-          s_scale[(kt % kScaleSlots) * kSlot + lane] = x;
-        }
-        convert(raw_k, base + L.k + st * TB, false);
-        mbar_arrive(bar(KFULL + st));
-        if (j + 1 < tiles) {
-          load_scales(tile0 + j + 1);
-          load(kcodes, tile0 + j + 1, raw_k);
-        }
-        if (kt >= 2 && !mbar_wait(bar(VEMPTY + st), ph, lim, p.status, abort_flag)) { ok = false; break; }
-        // a masked token's NaN stays out of the rows that do not see it
-        convert(raw_v, base + L.v + st * TB, t0 < s_in_lo[sp.v] || t0 + kTile > s_in_hi[sp.v]);
-        mbar_arrive(bar(VFULL + st));
-      }
-      u = seg_end;
-    }
-  } else if (lane == 0) {
-    // ================================================================ tensor core
-    const uint32_t id_qk = idesc_f16(kTile, 0), id_pv = idesc_f16(D, 1);
-    int64_t kt = 0;
-    int own[2] = {0, 0}, seg[2] = {0, 0};
+    constexpr int NS = raw_slots(D);
+    constexpr uint32_t BB = kKv8Block * D;             // bytes of a block
+    constexpr int LPR = D / 16, RPL = 32 / LPR;        // lanes a row, rows a step
+    const uint32_t ring = base + L.raw + w * NS * BB;
+    const int page = static_cast<int>(p.map.page), ppb = page / kKv8Block, num_pages = static_cast<int>(p.map.num_pages);
+    int kt = 0, issued = 0, used = 0;
     bool ok = true;
-    auto qk = [&](int rt, int st) {
-      const uint32_t a = base + L.q + rt * TB, bq = base + L.k + st * TB;
+    auto wait = [&](int id, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
+      return ok;
+    };
+    auto fetch = [&](const uint8_t* codes, int rec) {  // rec: of the block, the same in all lanes
+      const int sl = issued % NS;
+      ++issued;
+      if (lane == 0) {
+        mbar_expect_tx(bar(RAW + 4 * w + sl), BB);
+        bulk_load(ring + sl * BB, codes + static_cast<int64_t>(rec) * D, BB, bar(RAW + 4 * w + sl));
+      }
+      __syncwarp();
+    };
+    auto convert = [&](uint32_t dst, int row0, bool clean) {
+      const uint32_t src = ring + (used % NS) * BB + lane * 16;
+      uint4 x[BB / 512];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * 16384u + (k & 3) * 32u;
-        umma_f16(tmem + rt * 128, sw128_desc(a + off), sw128_desc(bq + off), id_qk, k > 0);
+      for (int k = 0; k < BB / 512; ++k) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
+                     : "r"(src + k * 512));
+        if (clean) {
+          x[k].x = e4m3_nan_to_zero(x[k].x);
+          x[k].y = e4m3_nan_to_zero(x[k].y);
+          x[k].z = e4m3_nan_to_zero(x[k].z);
+          x[k].w = e4m3_nan_to_zero(x[k].w);
+        }
+      }
+      // Lanes of a row's second 64 dims store their odd chunk first: the two parts of the operand
+      // tile lie in the same banks.
+      const int c = (lane % LPR) * 2;
+      const bool odd = D == 128 && (lane & 4);
+#pragma unroll
+      for (int k = 0; k < BB / 512; ++k) {
+        const int rr = row0 + k * RPL + lane / LPR;
+        const uint4 y = odd ? make_uint4(x[k].z, x[k].w, x[k].x, x[k].y) : x[k];
+        sts128(dst + tile_off(rr, c + odd), e4m3x2_to_h2(y.x), e4m3x2_to_h2(y.x >> 16), e4m3x2_to_h2(y.y), e4m3x2_to_h2(y.y >> 16));
+        sts128(dst + tile_off(rr, c + !odd), e4m3x2_to_h2(y.z), e4m3x2_to_h2(y.z >> 16), e4m3x2_to_h2(y.w), e4m3x2_to_h2(y.w >> 16));
       }
     };
-    for (int64_t u = u0; u < u1 && ok;) {
-      const Kv8Place sp = kv8_place_of(u, s_pref, VB, Hkv);
-      const int64_t seg_end = min(u1, u + sp.n - sp.tile);
-      const int tiles = static_cast<int>(seg_end - u);
-      const int gv = p.v0 + sp.v, r0 = (gv % p.RG) * kKv8PrefillRows;
-      const int nrt = r0 + kTile < R ? 2 : 1;
-      for (int j = -1; j < tiles && ok; ++j) {
-        // tile j's second product, then tile j + 1's first
-        const int64_t kn = kt + j + 1;
-        const int st = static_cast<int>((kt + j) & 1), stn = static_cast<int>(kn & 1);
-        for (int rt = 0; rt < nrt && ok; ++rt) {
-          if (j >= 0) {
-            if (rt == 0) ok = mbar_wait(bar(VFULL + st), ((kt + j) >> 1) & 1, lim, p.status, abort_flag);
-            if (ok) ok = mbar_wait(bar(PFULL + rt), own[rt] & 1, lim, p.status, abort_flag);
-            if (!ok) break;
-            ++own[rt];
-            tc_fence_after();
-            const uint32_t bv = base + L.v + st * TB;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              umma_f16_ts(tmem + 256 + rt * D, tmem + rt * 128 + k * 8, sw128_desc_t(bv + k * 2048u), id_pv, j > 0 || k > 0);
-            if (rt == nrt - 1) umma_commit(bar(VEMPTY + st));
-            if (j + 1 == tiles) umma_commit(bar(OFULL + rt));
-          } else {
-            ok = mbar_wait(bar(QFULL + rt), seg[rt] & 1, lim, p.status, abort_flag);
-            if (!ok) break;
-            ++seg[rt];
-            tc_fence_after();
+    for (int seg = 0; ok; ++seg) {
+      if (!wait(DFULL + (seg & 1), seg >> 1)) break;
+      const Run& run = s_meta[seg & 1].run;
+      const int tiles = run.tiles, b = run.b, head = run.h;
+      const int b_lo = run.lo / kKv8Block, b_hi = (run.hi - 1) / kKv8Block;
+      const int in_lo = run.in_lo, in_hi = run.in_hi;
+      int t0 = run.t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(MEMPTY + (seg & 1)));
+      if (tiles == 0) break;
+      const int32_t* row = p.map.table ? p.map.table + static_cast<int64_t>(b) * p.map.max_pages : nullptr;
+      // Lane k (of 8) holds the record of block k of a tile.  A block outside the visible tokens may
+      // have no page: the nearest visible one is taken.
+      auto ask = [&](int tile_t0, int& in) {           // its page
+        const int blk = min(max(tile_t0 / kKv8Block + lane % kBlocks, b_lo), b_hi), col = blk / ppb;
+        in = blk - col * ppb;
+        return row ? __ldg(row + col) : b;
+      };
+      auto record = [&](int id, int in) {
+        if (id < 0 || id >= num_pages) {
+          report_status(p.status, TQ_ERR_INVALID_ARG);
+          id = 0;
+        }
+        return (id * Hkv + head) * page + in * kKv8Block;          // (a side has fewer than 2^31 records)
+      };
+      auto block = [&](int rec, int k) { return __shfl_sync(0xffffffffu, rec, w + 4 * k); };
+      auto load_scales = [&](int rec) {      // lanes 0..7 key scales, 8..15 value scales
+        return w == 0 && lane < 2 * kBlocks ? __ldg((lane < kBlocks ? p.kscales : p.vscales) + rec / kKv8Block) : 0.f;
+      };
+      int in, rec = ask(t0, in);
+      rec = record(rec, in);
+      float scale = load_scales(rec);
+      fetch(kcodes, block(rec, 0));
+      fetch(kcodes, block(rec, 1));
+      if (NS == 4) {
+        fetch(vcodes, block(rec, 0));
+        fetch(vcodes, block(rec, 1));
+      }
+      int id = ask(t0 + kTile, in);          // (past the run: clamped to the visible tokens)
+      int E = 1;                             // largest value scale so far
+      for (int j = 0; j < tiles && ok; ++j, ++kt, t0 += kTile) {
+        const int st = kt & 1;
+        const uint32_t ph = static_cast<uint32_t>((kt >> 1) - 1);
+        const bool more = j + 1 < tiles;
+        const int next = record(id, in);
+        id = ask(t0 + 2 * kTile, in);
+        if (kt >= 2 && !wait(KEMPTY + st, ph)) break;
+        if (w == 0) {
+          const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu);
+          E = max(E, __reduce_max_sync(0xffffffffu, lane >= kBlocks && lane < 2 * kBlocks ? e : 0));
+          float* slot = s_scale + (kt % kScaleSlots) * kSlot;
+          if (lane < kBlocks) slot[lane] = scale;
+          else if (lane < 2 * kBlocks) {     // f: exponent of the block's probabilities
+            const int f = kHead + max(e - E, -100);
+            slot[lane] = static_cast<float>(f);
+            slot[lane + kBlocks] = __uint_as_float(static_cast<uint32_t>(127 - f) << 23);
+          } else if (lane == 2 * kBlocks) {
+            slot[3 * kBlocks] = static_cast<float>(E);
           }
-          if (j + 1 < tiles) {
-            if (rt == 0) ok = mbar_wait(bar(KFULL + stn), (kn >> 1) & 1, lim, p.status, abort_flag);
-            if (!ok) break;
+          if (more) scale = load_scales(next);
+        }
+        // a masked token's NaN stays out of the rows that do not see it (in values; scores are replaced)
+        const bool clean = t0 < in_lo || t0 + kTile > in_hi;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          if (side == 1 && kt >= 2 && !wait(VEMPTY + st, ph)) break;
+          const uint32_t dst = base + (side ? L.v : L.k) + st * TB;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (!wait(RAW + 4 * w + used % NS, used / NS)) break;
+            if (side == 1 && clean) convert(dst, (w + 4 * k) * kKv8Block, true);
+            else convert(dst, (w + 4 * k) * kKv8Block, false);
+            ++used;
+            __syncwarp();
+            // the block NS on takes the slot
+            if (NS == 2 && side == 0) fetch(vcodes, block(rec, k));
+            else if (more && NS == 2) fetch(kcodes, block(next, k));
+            else if (more) fetch(side ? vcodes : kcodes, block(next, k));
+          }
+          if (!ok) break;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(bar((side ? VFULL : KFULL) + st));
+        }
+        rec = next;
+      }
+    }
+    // copies still in flight land before the CTA ends (none, unless a wait gave up)
+    for (; used < issued; ++used)
+      for (long long i = 0; !mbar_try(bar(RAW + 4 * w + used % NS), (used / NS) & 1) && i < kDrainLimit; ++i) {}
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 12) {
+      // ============================================================== tensor core
+      // The whole warp waits; one lane issues.  The row tiles' products alternate, which also keeps
+      // their softmax half a period apart.
+      const uint32_t id_qk = idesc_f16(kTile, 0), id_pv = idesc_f16(D, 1);
+      const bool leader = elect_one();
+      int kt = 0;
+      uint32_t own = 0, seg = 0;             // bit rt: parity of the row tile's tiles and runs
+      bool ok = true;
+      auto wait = [&](int id, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
+        return ok;
+      };
+      for (int sg = 0; ok; ++sg) {
+        if (!wait(DFULL + (sg & 1), sg >> 1)) break;
+        const int tiles = s_meta[sg & 1].run.tiles, nrt = s_meta[sg & 1].run.r0 + kTile < R ? 2 : 1;
+        __syncwarp();
+        if (leader) mbar_arrive(bar(MEMPTY + (sg & 1)));
+        if (tiles == 0) break;
+        for (int j = -1; j < tiles && ok; ++j) {
+          // tile j's second product, then tile j + 1's first
+          const int kn = kt + j + 1;
+          const int st = (kt + j) & 1, stn = kn & 1;
+          if (j >= 0) wait(VFULL + st, (kt + j) >> 1);
+          if (j + 1 < tiles) wait(KFULL + stn, kn >> 1);
+          const uint64_t dv = sw128_desc_t(base + L.v + st * TB), dk = sw128_desc(base + L.k + stn * TB);
+#pragma unroll 1
+          for (int rt = 0; rt < nrt && ok; ++rt) {
+            const uint32_t ts = tmem + rt * 128, to = tmem + 256 + rt * D;
+            if (j >= 0) {
+              if (!wait(PHALF + rt, own >> rt)) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_f16_ts(to, ts + k * 8, dv + k * (2048u >> 4), id_pv, j > 0 || k > 0);
+              }
+              __syncwarp();
+              if (!wait(PFULL + rt, own >> rt)) break;
+              own ^= 1u << rt;
+            } else {
+              if (!wait(QFULL + rt, seg >> rt)) break;
+              seg ^= 1u << rt;
+            }
             tc_fence_after();
-            qk(rt, stn);
-            umma_commit(bar(SFULL + rt));
-            if (rt == nrt - 1) umma_commit(bar(KEMPTY + stn));
+            if (leader) {
+              if (j >= 0) {
+#pragma unroll
+                for (int k = 4; k < 8; ++k) umma_f16_ts(to, ts + k * 8, dv + k * (2048u >> 4), id_pv, 1);
+              }
+              if (j + 1 < tiles) {
+                const uint64_t dq = sw128_desc(base + L.q + rt * TB);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t off = ((k >> 2) * 16384u + (k & 3) * 32u) >> 4;
+                  umma_f16(ts, dq + off, dk + off, id_qk, k > 0);
+                }
+                umma_commit(bar(SFULL + rt));
+                if (rt == nrt - 1) umma_commit(bar(KEMPTY + stn));
+              } else {
+                umma_commit(bar(OFULL + rt));
+              }
+              if (j >= 0 && rt == nrt - 1) umma_commit(bar(VEMPTY + st));
+            }
+            __syncwarp();
           }
         }
+        kt += tiles;
       }
-      kt += tiles;
-      u = seg_end;
+      // all products end before tensor memory is given back
+      if (leader) {
+        const uint32_t end_bar = base + L.misc + 32;
+        mbar_init(end_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        umma_commit(end_bar);
+        for (long long i = 0; !mbar_try(end_bar, 0) && i < kDrainLimit; ++i) {}
+      }
+      __syncwarp();
+    } else {
+      // ============================================================== runs, and what their rows see
+      const int lt = tid - 13 * 32;
+      int seg = 0;
+      for (int64_t u = u0;;) {
+        Run run{};
+        int len = 0;
+        if (u < u1) {
+          run = run_at(u, u1, s_pref, VB, Hkv);
+          u += run.units;
+          if (run.tiles == 0) continue;
+          const int gv = p.v0 + run.v;
+          run.b = gv / p.RG;
+          run.r0 = (gv - run.b * p.RG) * kKv8PrefillRows;
+          len = kv8_len(p.sc.kv_lens, run.b, p.map.cap, nullptr);
+          group_range(run.b, run.r0, len, run.lo, run.hi, run.in_lo, run.in_hi);
+          run.t0 = (run.lo / kTile + run.tile) * kTile;
+        }
+        const int mb = seg & 1;
+        RowMeta& meta = s_meta[mb];
+        if (seg >= 2 && !mbar_wait(bar(MEMPTY + mb), ((seg >> 1) - 1) & 1, lim, p.status, abort_flag)) break;
+        ++seg;
+        if (lt == 0) meta.run = run;
+        if (run.tiles > 0) {
+          const int b = run.b;
+          for (int rr = lt; rr < kKv8PrefillRows; rr += kScouts) {
+            const int r = run.r0 + rr;
+            int lo = 0, hi = INT32_MAX, pos = 0;
+            float slope = 0.f;
+            int i = -1, hq = 0;
+            if (r < R) {
+              i = r / p.G;
+              hq = run.h * p.G + r - i * p.G;
+              kv8_range(p.sc, b, i, p.T, len, lo, hi, pos);
+              if (GEN && p.sc.slopes) slope = __ldg(p.sc.slopes + hq) * kLog2E;
+            }
+            meta.lo[rr] = lo;
+            meta.hi[rr] = hi;
+            meta.pos[rr] = pos;
+            meta.slope[rr] = slope;
+            meta.i[rr] = i;
+            meta.hq[rr] = hq;
+          }
+        }
+        mbar_arrive(bar(DFULL + mb));
+        if (run.tiles == 0) break;
+      }
     }
-    // all products end before tensor memory is given back
-    const uint32_t end_bar = base + L.misc + 48;
-    mbar_init(end_bar, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    umma_commit(end_bar);
-    for (long long i = 0; !mbar_try(end_bar, 0) && i < kDrainLimit; ++i) {}
   }
   tc_fence_before();
   __syncthreads();
@@ -563,19 +846,16 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   }
 }
 
-// Joins the partial results of a (256-row group, key head) that several CTAs worked on; one warp
-// a row.  Groups with no visible token get zeros.
+// Joins the partial results of a (256-row group, key head) that several CTAs worked on, one warp a
+// row: out = sum_c w_c out_c / sum_c w_c, w_c = 2^(lse_c - max).  Blocks x: the CTAs' boundaries.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const Kv8AttnParams p) {
   pdl_wait();
   pdl_trigger();
-  const int Hkv = p.map.Hkv, v = blockIdx.x / Hkv, h = blockIdx.x - v * Hkv;
-  const int64_t per = __ldg(reinterpret_cast<const int64_t*>(p.plan));
-  const int t0 = __ldg(p.plan + kKv8PlanHead + v), n = __ldg(p.plan + kKv8PlanHead + v + 1) - t0;
-  const int64_t u = static_cast<int64_t>(t0) * Hkv + static_cast<int64_t>(h) * n;
-  const int c0 = static_cast<int>(u / per), c1 = n ? static_cast<int>((u + n - 1) / per) : c0;
-  if (n && c0 == c1) return;
-  const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8PrefillRows, R = p.T * p.G;
+  const int4 split = __ldcg(reinterpret_cast<const int4*>(p.plan) + blockIdx.x + 1);
+  if (split.x < 0) return;
+  const int h = split.y, c0 = split.z, c1 = split.w;
+  const int gv = p.v0 + split.x, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8PrefillRows, R = p.T * p.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int PL = D / 32;
   const int rl = blockIdx.y * 8 + warp;
@@ -586,18 +866,16 @@ __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const Kv8AttnPara
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.f;
   auto prow = [&](int c) { return static_cast<int64_t>(c * 2 + (c == c0 ? 1 : 0)) * kKv8PrefillRows + rl; };
-  if (n) {
-    for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldg(p.part_lse + prow(c)));
-    mx = warp_max(mx);
-    if (mx > -INFINITY)
-      for (int c = c0; c <= c1; ++c) {
-        const float w = ex2(__ldg(p.part_lse + prow(c)) - mx);
-        sum += w;
-        const float* src = p.part_o + prow(c) * D + lane * PL;
+  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.part_lse + prow(c)));
+  mx = warp_max(mx);
+  if (mx > -INFINITY)
+    for (int c = c0; c <= c1; ++c) {
+      const float w = ex2(__ldcg(p.part_lse + prow(c)) - mx);
+      sum += w;
+      const float* src = p.part_o + prow(c) * D + lane * PL;
 #pragma unroll
-        for (int k = 0; k < PL; ++k) o[k] += w * __ldg(src + k);
-      }
-  }
+      for (int k = 0; k < PL; ++k) o[k] += w * __ldcg(src + k);
+    }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
 #pragma unroll
@@ -612,12 +890,16 @@ template <int D, bool GEN>
 cudaError_t go(const uint8_t* kc, const uint8_t* vc, const Kv8AttnParams& p, int grid, cudaStream_t s) {
   auto k = kv8_prefill_kernel<D, GEN>;
   constexpr uint32_t smem = prefill_smem(D).total;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the roles' register shares must fit what the launch has, or their exchange would not end
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, k);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(grid), dim3(kThreads), smem, s, kc, vc, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_prefill_join_kernel<D>, dim3(static_cast<unsigned>(p.VB) * p.map.Hkv, kKv8PrefillRows / 8), dim3(256), 0,
-                    s, p);
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_pdl(kv8_prefill_join_kernel<D>, dim3(grid - 1, kKv8PrefillRows / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
