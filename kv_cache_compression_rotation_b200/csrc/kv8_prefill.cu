@@ -41,9 +41,9 @@ constexpr int kScaleSlots = 4;               // tiles whose scales are kept: a s
 constexpr int kSlot = 3 * kBlocks + 4;       // key scales, exponents f of the probabilities, 2^-f, E
 constexpr int kRunCost = 2;                  // what a run costs beside its tiles, in tiles
 // Registers a thread of the roles' warpgroups; the launch has 128 for each of 512 threads.
-constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsRest = 56, kRegsLaunch = 128;
+constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsRest = 48, kRegsLaunch = 128;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
-constexpr int kScouts = 96;                  // threads of the three warps that prepare runs
+constexpr int kScouts = 64;                  // threads of the two warps that prepare runs
 
 // A run: tiles [tile, tile + tiles) of the n of key head h of virtual sequence v, which is rows r0 ..
 // of sequence b; tile 0 of the run starts at token t0.  tiles = 0: no more.
@@ -60,11 +60,8 @@ struct RowMeta {                             // of 256 rows
   int i[kKv8PrefillRows], hq[kKv8PrefillRows];       // query and head; i = -1: no row
 };
 
-// Blocks of codes on their way, for each converting warp.
-__host__ __device__ constexpr int raw_slots(int D) { return D == 64 ? 4 : 2; }
-
 struct PrefillSmem {
-  uint32_t q, k, v, raw, meta, scales, bars, pref, misc, total;
+  uint32_t q, k, v, meta, scales, bars, pref, misc, total;
 };
 __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   PrefillSmem L{};
@@ -73,10 +70,9 @@ __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   L.q = at; at += 2 * tile;
   L.k = at; at += 2 * tile;
   L.v = at; at += 2 * tile;
-  L.raw = at; at += 4 * raw_slots(D) * kKv8Block * D;
   L.meta = at; at += 2 * sizeof(RowMeta);
   L.scales = at; at += kScaleSlots * kSlot * 4;
-  L.bars = at; at += 38 * 8;
+  L.bars = at; at += 26 * 8;
   L.pref = at; at += (kKv8PrefillMaxVB + 4) * 4;
   L.misc = at; at += 64;
   L.total = at + 1024;
@@ -84,7 +80,7 @@ __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
 }
 static_assert(prefill_smem(128).total <= 232448, "shared memory");
 
-enum : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, OFULL = 12, QFULL = 14, MEMPTY = 16, DFULL = 18, PHALF = 20, RAW = 22 /* + 4 warp + slot */ };
+enum : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10, OFULL = 12, QFULL = 14, MEMPTY = 16, DFULL = 18, PHALF = 20, KRAW = 22, VRAW = 24 };
 
 // Operand tile of 128 rows of D halves: D / 64 parts of [128][64], 16-byte chunks XORed with the
 // row within 8.  Byte offset of chunk c (8 halves) of row r.
@@ -202,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict__ vcodes, const Kv8AttnParams p) {
   constexpr PrefillSmem L = prefill_smem(D);
   constexpr uint32_t TB = kTile * D * 2;     // bytes of an operand tile
+  constexpr uint32_t BB = kKv8Block * D;     // bytes of a block's codes, which arrive
+  constexpr uint32_t kRaw = D == 128 ? 16384u : 0u;    // there in the tile, and 2048 further for each block
   extern __shared__ unsigned char psm_raw[];
   const uint32_t raw = smem_u32(psm_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -225,11 +223,12 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       mbar_init(bar(PFULL + i), 128);
       mbar_init(bar(OFULL + i), 1);
       mbar_init(bar(QFULL + i), 128);
-      mbar_init(bar(MEMPTY + i), 256 + 4 + 1);         // softmax threads, converting and issuing warps
+      mbar_init(bar(MEMPTY + i), 256 + 4 + 1 + 1);     // softmax threads; converting, issuing and fetching warps
       mbar_init(bar(PHALF + i), 128);
       mbar_init(bar(DFULL + i), kScouts);
+      mbar_init(bar(KRAW + i), 1);
+      mbar_init(bar(VRAW + i), 1);
     }
-    for (int i = 0; i < 16; ++i) mbar_init(bar(RAW + i), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -572,144 +571,72 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   } else if (warp < 12) {
     // ================================================================ codes to halves
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    // Warp w takes blocks w and w + 4 of each tile's keys, then of its values; its blocks of codes
-    // arrive in a ring of its own.
+    // Warp w takes blocks w and w + 4 of each tile.  A block's codes stand where its halves will
+    // (in the operand's last 64 dims).
     const int w = warp - 8;
-    constexpr int NS = raw_slots(D);
-    constexpr uint32_t BB = kKv8Block * D;             // bytes of a block
-    constexpr int LPR = D / 16, RPL = 32 / LPR;        // lanes a row, rows a step
-    const uint32_t ring = base + L.raw + w * NS * BB;
-    const int page = static_cast<int>(p.map.page), ppb = page / kKv8Block, num_pages = static_cast<int>(p.map.num_pages);
-    int kt = 0, issued = 0, used = 0;
+    constexpr int LPR = D / 16, RPL = 32 / LPR, NL = BB / 512;       // lanes a row, rows a step, steps a block
+    int kt = 0;
     bool ok = true;
     auto wait = [&](int id, uint32_t parity) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
       return ok;
     };
-    auto fetch = [&](const uint8_t* codes, int rec) {  // rec: of the block, the same in all lanes
-      const int sl = issued % NS;
-      ++issued;
-      if (lane == 0) {
-        mbar_expect_tx(bar(RAW + 4 * w + sl), BB);
-        bulk_load(ring + sl * BB, codes + static_cast<int64_t>(rec) * D, BB, bar(RAW + 4 * w + sl));
-      }
-      __syncwarp();
-    };
-    auto convert = [&](uint32_t dst, int row0, bool clean) {
-      const uint32_t src = ring + (used % NS) * BB + lane * 16;
-      uint4 x[BB / 512];
+    auto convert = [&](int side, bool clean) {
+      const int st = kt & 1;
+      if (!wait((side ? VRAW : KRAW) + st, kt >> 1)) return;
+      const uint32_t dst = base + (side ? L.v : L.k) + st * TB;
+      uint4 x[2][NL];
 #pragma unroll
-      for (int k = 0; k < BB / 512; ++k) {
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
-                     : "r"(src + k * 512));
-        if (clean) {
-          x[k].x = e4m3_nan_to_zero(x[k].x);
-          x[k].y = e4m3_nan_to_zero(x[k].y);
-          x[k].z = e4m3_nan_to_zero(x[k].z);
-          x[k].w = e4m3_nan_to_zero(x[k].w);
-        }
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < NL; ++k)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(x[b][k].x), "=r"(x[b][k].y), "=r"(x[b][k].z), "=r"(x[b][k].w)
+                       : "r"(dst + kRaw + (w + 4 * b) * 2048 + k * 512 + lane * 16));
+      __syncwarp();                          // (each lane's codes are read before any is overwritten)
+      if (clean) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int k = 0; k < NL; ++k) {
+            x[b][k].x = e4m3_nan_to_zero(x[b][k].x);
+            x[b][k].y = e4m3_nan_to_zero(x[b][k].y);
+            x[b][k].z = e4m3_nan_to_zero(x[b][k].z);
+            x[b][k].w = e4m3_nan_to_zero(x[b][k].w);
+          }
       }
       // Lanes of a row's second 64 dims store their odd chunk first: the two parts of the operand
       // tile lie in the same banks.
       const int c = (lane % LPR) * 2;
       const bool odd = D == 128 && (lane & 4);
 #pragma unroll
-      for (int k = 0; k < BB / 512; ++k) {
-        const int rr = row0 + k * RPL + lane / LPR;
-        const uint4 y = odd ? make_uint4(x[k].z, x[k].w, x[k].x, x[k].y) : x[k];
-        sts128(dst + tile_off(rr, c + odd), e4m3x2_to_h2(y.x), e4m3x2_to_h2(y.x >> 16), e4m3x2_to_h2(y.y), e4m3x2_to_h2(y.y >> 16));
-        sts128(dst + tile_off(rr, c + !odd), e4m3x2_to_h2(y.z), e4m3x2_to_h2(y.z >> 16), e4m3x2_to_h2(y.w), e4m3x2_to_h2(y.w >> 16));
-      }
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+          const int rr = (w + 4 * b) * kKv8Block + k * RPL + lane / LPR;
+          const uint4 a = x[b][k], y = odd ? make_uint4(a.z, a.w, a.x, a.y) : a;
+          sts128(dst + tile_off(rr, c + odd), e4m3x2_to_h2(y.x), e4m3x2_to_h2(y.x >> 16), e4m3x2_to_h2(y.y),
+                 e4m3x2_to_h2(y.y >> 16));
+          sts128(dst + tile_off(rr, c + !odd), e4m3x2_to_h2(y.z), e4m3x2_to_h2(y.z >> 16), e4m3x2_to_h2(y.w),
+                 e4m3x2_to_h2(y.w >> 16));
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(bar((side ? VFULL : KFULL) + st));
     };
     for (int seg = 0; ok; ++seg) {
       if (!wait(DFULL + (seg & 1), seg >> 1)) break;
       const Run& run = s_meta[seg & 1].run;
-      const int tiles = run.tiles, b = run.b, head = run.h;
-      const int b_lo = run.lo / kKv8Block, b_hi = (run.hi - 1) / kKv8Block;
-      const int in_lo = run.in_lo, in_hi = run.in_hi;
+      const int tiles = run.tiles, in_lo = run.in_lo, in_hi = run.in_hi;
       int t0 = run.t0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(MEMPTY + (seg & 1)));
       if (tiles == 0) break;
-      const int32_t* row = p.map.table ? p.map.table + static_cast<int64_t>(b) * p.map.max_pages : nullptr;
-      // Lane k (of 8) holds the record of block k of a tile.  A block outside the visible tokens may
-      // have no page: the nearest visible one is taken.
-      auto ask = [&](int tile_t0, int& in) {           // its page
-        const int blk = min(max(tile_t0 / kKv8Block + lane % kBlocks, b_lo), b_hi), col = blk / ppb;
-        in = blk - col * ppb;
-        return row ? __ldg(row + col) : b;
-      };
-      auto record = [&](int id, int in) {
-        if (id < 0 || id >= num_pages) {
-          report_status(p.status, TQ_ERR_INVALID_ARG);
-          id = 0;
-        }
-        return (id * Hkv + head) * page + in * kKv8Block;          // (a side has fewer than 2^31 records)
-      };
-      auto block = [&](int rec, int k) { return __shfl_sync(0xffffffffu, rec, w + 4 * k); };
-      auto load_scales = [&](int rec) {      // lanes 0..7 key scales, 8..15 value scales
-        return w == 0 && lane < 2 * kBlocks ? __ldg((lane < kBlocks ? p.kscales : p.vscales) + rec / kKv8Block) : 0.f;
-      };
-      int in, rec = ask(t0, in);
-      rec = record(rec, in);
-      float scale = load_scales(rec);
-      fetch(kcodes, block(rec, 0));
-      fetch(kcodes, block(rec, 1));
-      if (NS == 4) {
-        fetch(vcodes, block(rec, 0));
-        fetch(vcodes, block(rec, 1));
-      }
-      int id = ask(t0 + kTile, in);          // (past the run: clamped to the visible tokens)
-      int E = 1;                             // largest value scale so far
       for (int j = 0; j < tiles && ok; ++j, ++kt, t0 += kTile) {
-        const int st = kt & 1;
-        const uint32_t ph = static_cast<uint32_t>((kt >> 1) - 1);
-        const bool more = j + 1 < tiles;
-        const int next = record(id, in);
-        id = ask(t0 + 2 * kTile, in);
-        if (kt >= 2 && !wait(KEMPTY + st, ph)) break;
-        if (w == 0) {
-          const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu);
-          E = max(E, __reduce_max_sync(0xffffffffu, lane >= kBlocks && lane < 2 * kBlocks ? e : 0));
-          float* slot = s_scale + (kt % kScaleSlots) * kSlot;
-          if (lane < kBlocks) slot[lane] = scale;
-          else if (lane < 2 * kBlocks) {     // f: exponent of the block's probabilities
-            const int f = kHead + max(e - E, -100);
-            slot[lane] = static_cast<float>(f);
-            slot[lane + kBlocks] = __uint_as_float(static_cast<uint32_t>(127 - f) << 23);
-          } else if (lane == 2 * kBlocks) {
-            slot[3 * kBlocks] = static_cast<float>(E);
-          }
-          if (more) scale = load_scales(next);
-        }
-        // a masked token's NaN stays out of the rows that do not see it (in values; scores are replaced)
-        const bool clean = t0 < in_lo || t0 + kTile > in_hi;
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          if (side == 1 && kt >= 2 && !wait(VEMPTY + st, ph)) break;
-          const uint32_t dst = base + (side ? L.v : L.k) + st * TB;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (!wait(RAW + 4 * w + used % NS, used / NS)) break;
-            if (side == 1 && clean) convert(dst, (w + 4 * k) * kKv8Block, true);
-            else convert(dst, (w + 4 * k) * kKv8Block, false);
-            ++used;
-            __syncwarp();
-            // the block NS on takes the slot
-            if (NS == 2 && side == 0) fetch(vcodes, block(rec, k));
-            else if (more && NS == 2) fetch(kcodes, block(next, k));
-            else if (more) fetch(side ? vcodes : kcodes, block(next, k));
-          }
-          if (!ok) break;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          mbar_arrive(bar((side ? VFULL : KFULL) + st));
-        }
-        rec = next;
+        convert(0, false);
+        // a masked token's NaN stays out of the rows that do not see it (scores are replaced)
+        if (ok) convert(1, t0 < in_lo || t0 + kTile > in_hi);
       }
     }
-    // copies still in flight land before the CTA ends (none, unless a wait gave up)
-    for (; used < issued; ++used)
-      for (long long i = 0; !mbar_try(bar(RAW + 4 * w + used % NS), (used / NS) & 1) && i < kDrainLimit; ++i) {}
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 12) {
@@ -760,6 +687,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
               if (j >= 0) {
 #pragma unroll
                 for (int k = 4; k < 8; ++k) umma_f16_ts(to, ts + k * 8, dv + k * (2048u >> 4), id_pv, 1);
+                if (rt == nrt - 1) umma_commit(bar(VEMPTY + st));
               }
               if (j + 1 < tiles) {
                 const uint64_t dq = sw128_desc(base + L.q + rt * TB);
@@ -773,7 +701,6 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
               } else {
                 umma_commit(bar(OFULL + rt));
               }
-              if (j >= 0 && rt == nrt - 1) umma_commit(bar(VEMPTY + st));
             }
             __syncwarp();
           }
@@ -789,6 +716,80 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         for (long long i = 0; !mbar_try(end_bar, 0) && i < kDrainLimit; ++i) {}
       }
       __syncwarp();
+    } else if (warp == 15) {
+      // ============================================================== codes and scales from the cache
+      // A tile's codes are asked for as soon as the products of two tiles before are done.
+      const int page = static_cast<int>(p.map.page), ppb = page / kKv8Block, num_pages = static_cast<int>(p.map.num_pages);
+      int kt = 0, asked[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](int id, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
+        return ok;
+      };
+      for (int seg = 0; ok; ++seg) {
+        if (!wait(DFULL + (seg & 1), seg >> 1)) break;
+        const Run& run = s_meta[seg & 1].run;
+        const int tiles = run.tiles, b = run.b, head = run.h;
+        const int b_lo = run.lo / kKv8Block, b_hi = (run.hi - 1) / kKv8Block;
+        int blk = run.t0 / kKv8Block + lane % kBlocks;       // lane k (of 8): block k of the tile
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(MEMPTY + (seg & 1)));
+        if (tiles == 0) break;
+        const int32_t* row = p.map.table ? p.map.table + static_cast<int64_t>(b) * p.map.max_pages : nullptr;
+        int in;
+        auto ask = [&]() {                     // the block's page and its place there
+          // a block outside the visible tokens may have no page: the nearest visible one is taken
+          const int c = min(max(blk, b_lo), b_hi), col = c / ppb;
+          in = c - col * ppb;
+          blk += kBlocks;
+          return row ? __ldg(row + col) : b;
+        };
+        int id = ask();
+        int E = 1;                             // largest value scale so far
+        for (int j = 0; j < tiles; ++j, ++kt) {
+          if (id < 0 || id >= num_pages) {
+            report_status(p.status, TQ_ERR_INVALID_ARG);
+            id = 0;
+          }
+          const int rec = (id * Hkv + head) * page + in * kKv8Block;         // (a side has fewer than 2^31 records)
+          // lanes 0..7: key scales, 8..15: value scales
+          const float scale = lane < 2 * kBlocks ? __ldg((lane < kBlocks ? p.kscales : p.vscales) + rec / kKv8Block) : 0.f;
+          id = ask();
+          const int st = kt & 1;
+#pragma unroll 1
+          for (int side = 0; side < 2 && ok; ++side) {
+            if (kt >= 2 && !wait((side ? VEMPTY : KEMPTY) + st, (kt >> 1) - 1)) break;
+            const uint32_t full = bar((side ? VRAW : KRAW) + st);
+            if (side == 0) {
+              // The scales' slot is free: its last readers, the softmax of four tiles before, are done,
+              // because the first product of two tiles before is.
+              const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu);
+              E = max(E, __reduce_max_sync(0xffffffffu, lane >= kBlocks && lane < 2 * kBlocks ? e : 0));
+              float* slot = s_scale + (kt % kScaleSlots) * kSlot;
+              if (lane < kBlocks) slot[lane] = scale;
+              else if (lane < 2 * kBlocks) {   // f: exponent of the block's probabilities
+                const int f = kHead + max(e - E, -100);
+                slot[lane] = static_cast<float>(f);
+                slot[lane + kBlocks] = __uint_as_float(static_cast<uint32_t>(127 - f) << 23);
+              } else if (lane == 2 * kBlocks) {
+                slot[3 * kBlocks] = static_cast<float>(E);
+              }
+              __syncwarp();
+            }
+            if (lane == 0) mbar_expect_tx(full, kBlocks * BB);
+            __syncwarp();
+            if (lane < kBlocks)
+              bulk_load(base + (side ? L.v : L.k) + st * TB + kRaw + lane * 2048,
+                        (side ? vcodes : kcodes) + static_cast<int64_t>(rec) * D, BB, full);
+            ++asked[side];
+          }
+          if (!ok) break;
+        }
+      }
+      // copies still in flight land before the CTA ends (none, unless a wait gave up)
+      for (int side = 0; side < 2; ++side)
+        for (int k = max(0, asked[side] - 2); k < asked[side]; ++k)
+          for (long long i = 0; !mbar_try(bar((side ? VRAW : KRAW) + (k & 1)), (k >> 1) & 1) && i < kDrainLimit; ++i) {}
     } else {
       // ============================================================== runs, and what their rows see
       const int lt = tid - 13 * 32;
