@@ -43,7 +43,7 @@ constexpr int kRunCost = 2;                  // what a run costs beside its tile
 // Registers a thread of the roles' warpgroups; the launch has 128 for each of 512 threads.
 constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsRest = 48, kRegsLaunch = 128;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
-constexpr int kScouts = 64;                  // threads of the two warps that prepare runs
+constexpr int kScouts = 32;                  // the warp that prepares runs
 
 // A run: tiles [tile, tile + tiles) of the n of key head h of virtual sequence v, which is rows r0 ..
 // of sequence b; tile 0 of the run starts at token t0.  tiles = 0: no more.
@@ -130,6 +130,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
 __device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll
   for (int k = 0; k < 32; ++k) asm volatile("" : "+f"(v[k]));
+}
+
+// Bounded wait of a warp; one that gives up raises the flag, which ends the others' (the status is
+// reported at the end).  Kept short: its copies and the unrolled softmax share the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int limit, volatile int* abort_flag) {
+  bool done = false;
+#pragma unroll 1
+  for (int i = 0; i < limit; ++i) {
+    done = mbar_try(bar, parity);
+    if (done || *abort_flag) break;
+  }
+  if (__all_sync(0xffffffffu, done)) return true;
+  *abort_flag = 1;
+  return false;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -223,7 +237,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       mbar_init(bar(PFULL + i), 128);
       mbar_init(bar(OFULL + i), 1);
       mbar_init(bar(QFULL + i), 128);
-      mbar_init(bar(MEMPTY + i), 256 + 4 + 1 + 1);     // softmax threads; converting, issuing and fetching warps
+      mbar_init(bar(MEMPTY + i), 256 + 4 + 1 + 2);     // softmax threads; converting, issuing and fetching warps
       mbar_init(bar(PHALF + i), 128);
       mbar_init(bar(DFULL + i), kScouts);
       mbar_init(bar(KRAW + i), 1);
@@ -275,7 +289,8 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
   if (tid == 0) kv8_plan_split<kRunCost>(p.plan, u0, u1, per, s_pref, VB, Hkv);
   pdl_trigger();
-  const long long lim = p.wait_limit;
+  const int lim = static_cast<int>(min(p.wait_limit, static_cast<long long>(INT32_MAX)));
+  auto wait_for = [&](int id, uint32_t parity) { return wait_bar(bar(id), parity & 1u, lim, abort_flag); };
 
   if (warp < 8) {
     // ================================================================ softmax
@@ -335,7 +350,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     for (int seg = 0;; ++seg) {
       const RowMeta& meta = s_meta[seg & 1];
       const Run& run = meta.run;
-      if (!loaded) ok = __all_sync(0xffffffffu, mbar_wait(bar(DFULL + (seg & 1)), (seg >> 1) & 1, lim, p.status, abort_flag));
+      if (!loaded) ok = wait_for(DFULL + (seg & 1), (seg >> 1) & 1);
       const int tiles = run.tiles;
       if (!ok || tiles == 0) break;
       if (run.r0 + rt * kTile >= R) {        // this row tile is empty
@@ -352,7 +367,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       const float slope = GEN ? meta.slope[rr] : 0.f;
       float m = -INFINITY, l = 0.f, E = 1.f;
       for (int j = 0; j < tiles; ++j, ++kt, ++own, t0 += kTile) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + rt), own & 1, lim, p.status, abort_flag));
+        ok = wait_for(SFULL + rt, own & 1);
         if (!ok) break;
         tc_fence_after();
         // the row's scores stay in registers (the probabilities overwrite them in tensor memory)
@@ -501,12 +516,12 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       if (!ok) break;
       // ---- the next run's row of q is asked for before this run's result is waited for
       const RowMeta& after = s_meta[(seg & 1) ^ 1];
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(DFULL + ((seg + 1) & 1)), ((seg + 1) >> 1) & 1, lim, p.status, abort_flag));
+      ok = wait_for(DFULL + ((seg + 1) & 1), ((seg + 1) >> 1) & 1);
       if (!ok) break;
       loaded = true;
       load_q(after, after.run.tiles > 0 && after.run.r0 + rt * kTile < R);
       // ---- the run's result
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(OFULL + rt), oseg & 1, lim, p.status, abort_flag));
+      ok = wait_for(OFULL + rt, oseg & 1);
       if (!ok) break;
       ++oseg;
       tc_fence_after();
@@ -578,7 +593,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     int kt = 0;
     bool ok = true;
     auto wait = [&](int id, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
+      ok = wait_for(id, parity);
       return ok;
     };
     auto convert = [&](int side, bool clean) {
@@ -632,9 +647,9 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       if (lane == 0) mbar_arrive(bar(MEMPTY + (seg & 1)));
       if (tiles == 0) break;
       for (int j = 0; j < tiles && ok; ++j, ++kt, t0 += kTile) {
-        convert(0, false);
         // a masked token's NaN stays out of the rows that do not see it (scores are replaced)
-        if (ok) convert(1, t0 < in_lo || t0 + kTile > in_hi);
+#pragma unroll 1
+        for (int side = 0; side < 2 && ok; ++side) convert(side, side && (t0 < in_lo || t0 + kTile > in_hi));
       }
     }
   } else {
@@ -649,7 +664,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       uint32_t own = 0, seg = 0;             // bit rt: parity of the row tile's tiles and runs
       bool ok = true;
       auto wait = [&](int id, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
+        if (ok) ok = wait_for(id, parity);
         return ok;
       };
       for (int sg = 0; ok; ++sg) {
@@ -716,18 +731,18 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         for (long long i = 0; !mbar_try(end_bar, 0) && i < kDrainLimit; ++i) {}
       }
       __syncwarp();
-    } else if (warp == 15) {
+    } else if (warp >= 14) {
       // ============================================================== codes and scales from the cache
-      // A tile's codes are asked for as soon as the products of two tiles before are done.
+      // Warp 14 asks for keys, and all scales, warp 15 for values: a tile's codes as soon as the
+      // products of two tiles before are done.
+      const int side = warp - 14;
+      const uint8_t* codes = side ? vcodes : kcodes;
       const int page = static_cast<int>(p.map.page), ppb = page / kKv8Block, num_pages = static_cast<int>(p.map.num_pages);
-      int kt = 0, asked[2] = {0, 0};
+      int kt = 0;
       bool ok = true;
-      auto wait = [&](int id, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(id), parity & 1u, lim, p.status, abort_flag));
-        return ok;
-      };
-      for (int seg = 0; ok; ++seg) {
-        if (!wait(DFULL + (seg & 1), seg >> 1)) break;
+      for (int seg = 0;; ++seg) {
+        ok = wait_for(DFULL + (seg & 1), seg >> 1);
+        if (!ok) break;
         const Run& run = s_meta[seg & 1].run;
         const int tiles = run.tiles, b = run.b, head = run.h;
         const int b_lo = run.lo / kKv8Block, b_hi = (run.hi - 1) / kKv8Block;
@@ -744,55 +759,61 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
           blk += kBlocks;
           return row ? __ldg(row + col) : b;
         };
-        int id = ask();
-        int E = 1;                             // largest value scale so far
-        for (int j = 0; j < tiles; ++j, ++kt) {
+        auto record = [&](int id) {
           if (id < 0 || id >= num_pages) {
             report_status(p.status, TQ_ERR_INVALID_ARG);
             id = 0;
           }
-          const int rec = (id * Hkv + head) * page + in * kKv8Block;         // (a side has fewer than 2^31 records)
-          // lanes 0..7: key scales, 8..15: value scales
-          const float scale = lane < 2 * kBlocks ? __ldg((lane < kBlocks ? p.kscales : p.vscales) + rec / kKv8Block) : 0.f;
-          id = ask();
+          return (id * Hkv + head) * page + in * kKv8Block;          // (a side has fewer than 2^31 records)
+        };
+        auto load_scale = [&](int rec) {       // lanes 0..7: key scales, 8..15: value scales
+          return side == 0 && lane < 2 * kBlocks ? __ldg((lane < kBlocks ? p.kscales : p.vscales) + rec / kKv8Block) : 0.f;
+        };
+        int rec = record(ask());
+        float scale = load_scale(rec);
+        int id = ask();
+        int E = 1;                             // largest value scale so far
+        for (int j = 0; j < tiles; ++j, ++kt) {
           const int st = kt & 1;
-#pragma unroll 1
-          for (int side = 0; side < 2 && ok; ++side) {
-            if (kt >= 2 && !wait((side ? VEMPTY : KEMPTY) + st, (kt >> 1) - 1)) break;
-            const uint32_t full = bar((side ? VRAW : KRAW) + st);
-            if (side == 0) {
-              // The scales' slot is free: its last readers, the softmax of four tiles before, are done,
-              // because the first product of two tiles before is.
-              const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu);
-              E = max(E, __reduce_max_sync(0xffffffffu, lane >= kBlocks && lane < 2 * kBlocks ? e : 0));
-              float* slot = s_scale + (kt % kScaleSlots) * kSlot;
-              if (lane < kBlocks) slot[lane] = scale;
-              else if (lane < 2 * kBlocks) {   // f: exponent of the block's probabilities
-                const int f = kHead + max(e - E, -100);
-                slot[lane] = static_cast<float>(f);
-                slot[lane + kBlocks] = __uint_as_float(static_cast<uint32_t>(127 - f) << 23);
-              } else if (lane == 2 * kBlocks) {
-                slot[3 * kBlocks] = static_cast<float>(E);
-              }
-              __syncwarp();
+          if (kt >= 2 && !(ok = wait_for((side ? VEMPTY : KEMPTY) + st, (kt >> 1) - 1))) break;
+          if (side == 0) {
+            // The scales' slot is free: its last readers, the softmax of four tiles before, are done,
+            // because the first product of two tiles before is.
+            const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu);
+            E = max(E, __reduce_max_sync(0xffffffffu, lane >= kBlocks && lane < 2 * kBlocks ? e : 0));
+            float* slot = s_scale + (kt % kScaleSlots) * kSlot;
+            if (lane < kBlocks) slot[lane] = scale;
+            else if (lane < 2 * kBlocks) {     // f: exponent of the block's probabilities
+              const int f = kHead + max(e - E, -100);
+              slot[lane] = static_cast<float>(f);
+              slot[lane + kBlocks] = __uint_as_float(static_cast<uint32_t>(127 - f) << 23);
+            } else if (lane == 2 * kBlocks) {
+              slot[3 * kBlocks] = static_cast<float>(E);
             }
-            if (lane == 0) mbar_expect_tx(full, kBlocks * BB);
             __syncwarp();
-            if (lane < kBlocks)
-              bulk_load(base + (side ? L.v : L.k) + st * TB + kRaw + lane * 2048,
-                        (side ? vcodes : kcodes) + static_cast<int64_t>(rec) * D, BB, full);
-            ++asked[side];
           }
-          if (!ok) break;
+          // blocks that follow one another in the cache come in one copy (where they do in the tile: d = 128)
+          const uint32_t full = bar((side ? VRAW : KRAW) + st);
+          const int before = __shfl_up_sync(0xffffffffu, rec, 1);
+          const bool head_of = lane < kBlocks && (D == 64 || lane == 0 || rec != before + kKv8Block);
+          const uint32_t heads = __ballot_sync(0xffffffffu, head_of) | (1u << kBlocks);
+          const int len = __ffs(heads >> (lane + 1) % 32);
+          if (lane == 0) mbar_expect_tx(full, kBlocks * BB);
+          __syncwarp();
+          if (head_of)
+            bulk_load(base + (side ? L.v : L.k) + st * TB + kRaw + lane * 2048, codes + static_cast<int64_t>(rec) * D, len * BB, full);
+          rec = record(id);
+          scale = load_scale(rec);
+          id = ask();
         }
+        if (!ok) break;
       }
       // copies still in flight land before the CTA ends (none, unless a wait gave up)
-      for (int side = 0; side < 2; ++side)
-        for (int k = max(0, asked[side] - 2); k < asked[side]; ++k)
-          for (long long i = 0; !mbar_try(bar((side ? VRAW : KRAW) + (k & 1)), (k >> 1) & 1) && i < kDrainLimit; ++i) {}
+      for (int k = max(0, kt - 2); k < kt; ++k)
+        for (long long i = 0; !mbar_try(bar((side ? VRAW : KRAW) + (k & 1)), (k >> 1) & 1) && i < kDrainLimit; ++i) {}
     } else {
       // ============================================================== runs, and what their rows see
-      const int lt = tid - 13 * 32;
+      const int lt = lane;
       int seg = 0;
       for (int64_t u = u0;;) {
         Run run{};
@@ -810,7 +831,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         }
         const int mb = seg & 1;
         RowMeta& meta = s_meta[mb];
-        if (seg >= 2 && !mbar_wait(bar(MEMPTY + mb), ((seg >> 1) - 1) & 1, lim, p.status, abort_flag)) break;
+        if (seg >= 2 && !wait_for(MEMPTY + mb, (seg >> 1) - 1)) break;
         ++seg;
         if (lt == 0) meta.run = run;
         if (run.tiles > 0) {
@@ -841,6 +862,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag) report_status(p.status, kDevTimeout);
   if (warp == 12) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
