@@ -61,7 +61,7 @@ struct RowMeta {                             // of 256 rows
 };
 
 struct PrefillSmem {
-  uint32_t q, k, v, meta, scales, bars, pref, misc, total;
+  uint32_t q, k, v, stage, meta, scales, bars, pref, misc, total;
 };
 __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   PrefillSmem L{};
@@ -70,6 +70,7 @@ __host__ __device__ constexpr PrefillSmem prefill_smem(int D) {
   L.q = at; at += 2 * tile;
   L.k = at; at += 2 * tile;
   L.v = at; at += 2 * tile;
+  L.stage = at; at += 8 * 2048;              // results on their way out, 64 bytes of 32 rows a warp
   L.meta = at; at += 2 * sizeof(RowMeta);
   L.scales = at; at += kScaleSlots * kSlot * 4;
   L.bars = at; at += 26 * 8;
@@ -86,6 +87,12 @@ enum : int { KFULL = 0, KEMPTY = 2, VFULL = 4, VEMPTY = 6, SFULL = 8, PFULL = 10
 // row within 8.  Byte offset of chunk c (8 halves) of row r.
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return (c >> 3) * 16384u + r * 128u + (((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -181,14 +188,32 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return floats2(r);
 }
 
-// tanh for |z| <= 1/2: the series to z^11, whose next term is below 2^-21.
-__device__ __forceinline__ float2 tanh_small(float2 z) {
-  const float2 u = mul2(z, z);
-  float2 p = fma2(u, both(-1382.f / 155925.f), both(62.f / 2835.f));
-  p = fma2(u, p, both(-17.f / 315.f));
-  p = fma2(u, p, both(2.f / 15.f));
-  p = fma2(u, p, both(-1.f / 3.f));
-  return fma2(mul2(z, u), p, z);
+// out * tanh(in * x) of 16 values, |in * x| <= 1/2: the series to z^11, whose next term is below 2^-21.
+// Step by step for all, so that no step waits for the one before.
+__device__ __forceinline__ void tanh_small(float (&s)[32], int at, float in, float out) {
+  float2 z[8], u[8], q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) z[k] = mul2(pair(s[at + 2 * k], s[at + 2 * k + 1]), both(in));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u[k] = mul2(z[k], z[k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = fma2(u[k], both(-1382.f / 155925.f), both(62.f / 2835.f));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = fma2(u[k], q[k], both(-17.f / 315.f));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = fma2(u[k], q[k], both(2.f / 15.f));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = fma2(u[k], q[k], both(-1.f / 3.f));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) z[k] = mul2(z[k], both(out));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u[k] = mul2(z[k], u[k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 y = fma2(u[k], q[k], z[k]);
+    s[at + 2 * k] = y.x;
+    s[at + 2 * k + 1] = y.y;
+  }
 }
 
 // The run that starts at unit u of the line and ends at u1 or with its key head.  A key head takes
@@ -230,9 +255,9 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(KFULL + i), 128);
-      mbar_init(bar(KEMPTY + i), 1);
+      mbar_init(bar(KEMPTY + i), 4);
       mbar_init(bar(VFULL + i), 128);
-      mbar_init(bar(VEMPTY + i), 1);
+      mbar_init(bar(VEMPTY + i), 4);
       mbar_init(bar(SFULL + i), 1);
       mbar_init(bar(PFULL + i), 128);
       mbar_init(bar(OFULL + i), 1);
@@ -287,7 +312,6 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
   const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
   const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
-  if (tid == 0) kv8_plan_split<kRunCost>(p.plan, u0, u1, per, s_pref, VB, Hkv);
   pdl_trigger();
   const int lim = static_cast<int>(min(p.wait_limit, static_cast<long long>(INT32_MAX)));
   auto wait_for = [&](int id, uint32_t parity) { return wait_bar(bar(id), parity & 1u, lim, abort_flag); };
@@ -303,25 +327,33 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     const int rr = rt * kTile + row;
     const uint32_t qa = base + L.q + rt * TB;
     float rowc = 0.f;
-    uint4 qx[D / 8];                         // the next run's row of q, on its way
-    bool loaded = false;                     // the run was waited for, its q asked for
-    auto load_q = [&](const RowMeta& meta, bool want) {
-      const int i = want ? meta.i[rr] : -1;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(p.q) + meta.run.b * p.q_stride_b + meta.hq[rr] * p.q_stride_h + i * p.q_stride_t);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) qx[c] = i >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    bool asked = false;                      // the run was waited for, its q asked for
+    // The warp's 32 rows of q, each by D / 8 neighbouring lanes, to where they will stand as an operand.
+    auto ask_q = [&](const RowMeta& meta) {
+      constexpr int LPR = D / 8;
+      const int64_t at_b = meta.run.b * p.q_stride_b;
+#pragma unroll 4
+      for (int k = 0; k < LPR; ++k) {
+        const int r = (warp & 3) * 32 + k * (32 / LPR) + lane / LPR, c = lane % LPR;
+        const int i = max(meta.i[rt * kTile + r], 0);        // (a row that is none: another one's q, not used)
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + at_b + meta.hq[rt * kTile + r] * p.q_stride_h + i * p.q_stride_t;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(qa + tile_off(r, c)), "l"(src + c * 8) : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // The row divided by a power of two, its largest entry in [1, 2), as an operand.
-    auto store_q = [&]() {
+    // This thread's row divided by a power of two, its largest entry in [1, 2).
+    auto scale_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       auto unpack = [&](uint32_t w) {
         return bf ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
                   : __half22float2(*reinterpret_cast<const __half2*>(&w));
       };
       float mx = 0.f;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w[4] = {qx[c].x, qx[c].y, qx[c].z, qx[c].w};
+        const uint4 x = lds128(qa + tile_off(row, c));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = unpack(w[k]);
@@ -332,9 +364,10 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
       rowc = __uint_as_float(static_cast<uint32_t>(e) << 23) * fabsf(p.sc.scale_log2);
       if (p.sc.scale_log2 < 0.f) down = -down;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w[4] = {qx[c].x, qx[c].y, qx[c].z, qx[c].w};
+        const uint4 x = lds128(qa + tile_off(row, c));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         uint32_t y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -350,26 +383,33 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     for (int seg = 0;; ++seg) {
       const RowMeta& meta = s_meta[seg & 1];
       const Run& run = meta.run;
-      if (!loaded) ok = wait_for(DFULL + (seg & 1), (seg >> 1) & 1);
+      if (!asked) ok = wait_for(DFULL + (seg & 1), (seg >> 1) & 1);
       const int tiles = run.tiles;
       if (!ok || tiles == 0) break;
       if (run.r0 + rt * kTile >= R) {        // this row tile is empty
         kt += tiles;
-        loaded = false;
+        asked = false;
         mbar_arrive(bar(MEMPTY + (seg & 1)));
         continue;
       }
-      if (!loaded) load_q(meta, true);
-      store_q();
-      loaded = false;
+      if (!asked) ask_q(meta);
+      scale_q();
+      asked = false;
       int t0 = run.t0;
       const int lo = meta.lo[rr], hi = meta.hi[rr], pos = GEN ? meta.pos[rr] : 0;
       const float slope = GEN ? meta.slope[rr] : 0.f;
+      const bool last = rt == 1 || run.r0 + kTile >= R;
       float m = -INFINITY, l = 0.f, E = 1.f;
       for (int j = 0; j < tiles; ++j, ++kt, ++own, t0 += kTile) {
         ok = wait_for(SFULL + rt, own & 1);
         if (!ok) break;
         tc_fence_after();
+        // The last row tile's first product is done: so are all that read the keys, and the values of
+        // the tile before.
+        if (last && lane == 0) {
+          mbar_arrive(bar(KEMPTY + (kt & 1)));
+          if (j > 0) mbar_arrive(bar(VEMPTY + ((kt - 1) & 1)));
+        }
         // the row's scores stay in registers (the probabilities overwrite them in tensor memory)
         float s0[32], s1[32], s2[32], s3[32];
         tmem_ld32(ts, s0);
@@ -391,12 +431,8 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
                 far1 = fmaxf(far1, fabsf(s[16 + k]));
               }
               if (__all_sync(0xffffffffu, fmaxf(far * z0, far1 * z1) <= 0.5f)) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                  const float2 y = mul2(tanh_small(mul2(pair(s[k], s[k + 1]), both(k < 16 ? z0 : z1))), both(cap2));
-                  s[k] = y.x;
-                  s[k + 1] = y.y;
-                }
+                tanh_small(s, 0, z0, cap2);
+                tanh_small(s, 16, z1, cap2);
               } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) s[k] = cap2 * kv8_tanh(s[k] * (k < 16 ? z0 : z1));
@@ -518,12 +554,13 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       const RowMeta& after = s_meta[(seg & 1) ^ 1];
       ok = wait_for(DFULL + ((seg + 1) & 1), ((seg + 1) >> 1) & 1);
       if (!ok) break;
-      loaded = true;
-      load_q(after, after.run.tiles > 0 && after.run.r0 + rt * kTile < R);
+      asked = true;
+      if (after.run.tiles > 0 && after.run.r0 + rt * kTile < R) ask_q(after);
       // ---- the run's result
       ok = wait_for(OFULL + rt, oseg & 1);
       if (!ok) break;
       ++oseg;
+      if (last && lane == 0) mbar_arrive(bar(VEMPTY + ((kt - 1) & 1)));
       tc_fence_after();
       const bool whole = tiles == run.n;
       // O is in units of 2^(E - 127 - kHead); two factors, so that neither leaves the normal range
@@ -531,43 +568,53 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
       const float inv = l == 0.f ? 0.f : 1.f / (l * (1 << kHead));
       const float ls2 = l == 0.f ? -INFINITY : m + __log2f(l);
       const bool on = meta.i[rr] >= 0;
-      const int64_t at = (static_cast<int64_t>(run.b) * p.Hq + meta.hq[rr]) * p.T + meta.i[rr];
       const int slot = blockIdx.x * 2 + (run.tile == 0 ? 1 : 0);
-      mbar_arrive(bar(MEMPTY + (seg & 1)));  // (behind the last use of run and meta)
       const int64_t prow = static_cast<int64_t>(slot) * kKv8PrefillRows + rr;
+      auto out_row = [&](int rr) { return (static_cast<int64_t>(run.b) * p.Hq + meta.hq[rr]) * p.T + meta.i[rr]; };
       if (on) {
-        if (whole) { if (p.lse) p.lse[at] = ls2 * kLn2; }
+        if (whole) { if (p.lse) p.lse[out_row(rr)] = ls2 * kLn2; }
         else p.part_lse[prow] = ls2;
       }
+      // 64 bytes a row at a time, by way of shared memory, so that four lanes write them together
+      const uint32_t stage = base + L.stage + warp * 2048;
+      const int per = whole ? 32 : 16;       // dims
 #pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        float o[16];
-        tmem_ld16(to + 16 * c, o);
-        tmem_wait_ld();
+      for (int c = 0; c < D; c += per) {
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * inv * unit;
-        if (on && whole) {
-          uint32_t w[8];
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !whole) break;
+          float o[16];
+          tmem_ld16(to + c + 16 * h, o);
+          tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (bf) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
-              w[k] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-              w[k] = pack_h2(o[2 * k], o[2 * k + 1]);
+          for (int k = 0; k < 16; ++k) o[k] = o[k] * inv * unit;
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
+              w[8 * h + k] = bf ? *reinterpret_cast<const uint32_t*>(&y) : pack_h2(o[2 * k], o[2 * k + 1]);
             }
-          }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 16 * c);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else if (on) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 16 * c);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sts128(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 8 * k + (lane >> 2), x = lane & 3, ra = rt * kTile + (warp & 3) * 32 + r;
+          const uint4 v = lds128(stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
+          if (meta.i[ra] < 0) continue;
+          if (whole) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row(ra) * D + c)[x] = v;
+          else reinterpret_cast<uint4*>(p.part_o + (prow - lane + r) * D + c)[x] = v;
         }
         __syncwarp();
       }
+      mbar_arrive(bar(MEMPTY + (seg & 1)));  // (behind the last use of run and meta)
       tc_fence_before();                     // before the next run's products overwrite O
     }
     // ---- groups that see nothing
@@ -677,8 +724,9 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
           // tile j's second product, then tile j + 1's first
           const int kn = kt + j + 1;
           const int st = (kt + j) & 1, stn = kn & 1;
-          if (j >= 0) wait(VFULL + st, (kt + j) >> 1);
+          // (the converting warps are done with a tile's values before the next tile's keys)
           if (j + 1 < tiles) wait(KFULL + stn, kn >> 1);
+          else wait(VFULL + st, (kt + j) >> 1);
           const uint64_t dv = sw128_desc_t(base + L.v + st * TB), dk = sw128_desc(base + L.k + stn * TB);
 #pragma unroll 1
           for (int rt = 0; rt < nrt && ok; ++rt) {
@@ -702,7 +750,6 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
               if (j >= 0) {
 #pragma unroll
                 for (int k = 4; k < 8; ++k) umma_f16_ts(to, ts + k * 8, dv + k * (2048u >> 4), id_pv, 1);
-                if (rt == nrt - 1) umma_commit(bar(VEMPTY + st));
               }
               if (j + 1 < tiles) {
                 const uint64_t dq = sw128_desc(base + L.q + rt * TB);
@@ -712,7 +759,6 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
                   umma_f16(ts, dq + off, dk + off, id_qk, k > 0);
                 }
                 umma_commit(bar(SFULL + rt));
-                if (rt == nrt - 1) umma_commit(bar(KEMPTY + stn));
               } else {
                 umma_commit(bar(OFULL + rt));
               }
@@ -858,6 +904,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         mbar_arrive(bar(DFULL + mb));
         if (run.tiles == 0) break;
       }
+      if (lane == 0) kv8_plan_split<kRunCost>(p.plan, u0, u1, per, s_pref, VB, Hkv);
     }
   }
   tc_fence_before();
