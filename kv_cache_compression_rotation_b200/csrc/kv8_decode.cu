@@ -611,7 +611,8 @@ template <int D, int NT, int W>
 cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
   auto k = kv8_decode_kernel<D, NT, W>;
   constexpr uint32_t smem = decode_smem(D, NT).total;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = allow_smem(k, smem, seen);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(grid), dim3(kWarps * 32), smem, s, km, vm, p);
   if (e != cudaSuccess) return e;

@@ -4,9 +4,24 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace tq {
+
+// Allows kernel k `smem` bytes of dynamic shared memory, once a device (seen: bit of each device).
+template <typename K>
+cudaError_t allow_smem(K* k, int smem, std::atomic<uint64_t>& seen) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (seen.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct Kv8AppendParams {
   const void* x[2];                                   // new keys, new values

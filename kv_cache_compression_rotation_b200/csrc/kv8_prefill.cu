@@ -39,7 +39,9 @@ constexpr int kHead = 7;                     // P <= 2^(kLazy + kHead)
 constexpr int kScaleSlots = 4;               // tiles whose scales are kept: a slot is filled again when the
                                              // first product of the tile two before is done, so none in use
 constexpr int kSlot = 3 * kBlocks + 4;       // key scales, exponents f of the probabilities, 2^-f, E
-constexpr int kRunCost = 2;                  // what a run costs beside its tiles, in tiles
+// What a run costs beside its tiles, in tiles: q, the first copies, the result.  (8k tokens, causal, d = 128:
+// 775 us with 2, 589 with 4, 605 with 7; where the tiles cost more, capped d = 64: 114 with 2, 125 with 4.)
+__host__ __device__ constexpr int run_cost(bool gen) { return gen ? 2 : 4; }
 // Registers a thread of the roles' warpgroups; the launch has 128 for each of 512 threads.
 constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsRest = 48, kRegsLaunch = 128;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
@@ -217,16 +219,16 @@ __device__ __forceinline__ void tanh_small(float (&s)[32], int at, float in, flo
 }
 
 // The run that starts at unit u of the line and ends at u1 or with its key head.  A key head takes
-// kRunCost units and one for each tile.
-__device__ __forceinline__ Run run_at(int64_t u, int64_t u1, const int* pref, int VB, int Hkv) {
+// `cost` units and one for each tile.
+__device__ __forceinline__ Run run_at(int64_t u, int64_t u1, const int* pref, int VB, int Hkv, int cost) {
   const Kv8Place p = kv8_place_of(u, pref, VB, Hkv);
   Run r;
   r.v = p.v;
   r.h = p.h;
-  r.n = p.n - kRunCost;
+  r.n = p.n - cost;
   r.units = static_cast<int>(min(u1 - u, static_cast<int64_t>(p.n - p.tile)));
-  r.tile = max(0, p.tile - kRunCost);
-  r.tiles = max(0, p.tile + r.units - kRunCost) - r.tile;
+  r.tile = max(0, p.tile - cost);
+  r.tiles = max(0, p.tile + r.units - cost) - r.tile;
   r.b = r.r0 = r.t0 = r.lo = r.hi = r.in_lo = r.in_hi = 0;
   return r;
 }
@@ -301,7 +303,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
     const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, p.status);
     int lo, hi, in_lo, in_hi;
     group_range(b, r0, len, lo, hi, in_lo, in_hi);
-    if (lane == 0) s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile + kRunCost : 0;
+    if (lane == 0) s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile + run_cost(GEN) : 0;
   }
   __syncthreads();
   if (warp == 0) kv8_prefix(s_pref, VB);
@@ -865,7 +867,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         Run run{};
         int len = 0;
         if (u < u1) {
-          run = run_at(u, u1, s_pref, VB, Hkv);
+          run = run_at(u, u1, s_pref, VB, Hkv, run_cost(GEN));
           u += run.units;
           if (run.tiles == 0) continue;
           const int gv = p.v0 + run.v;
@@ -904,7 +906,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         mbar_arrive(bar(DFULL + mb));
         if (run.tiles == 0) break;
       }
-      if (lane == 0) kv8_plan_split<kRunCost>(p.plan, u0, u1, per, s_pref, VB, Hkv);
+      if (lane == 0) kv8_plan_split<run_cost(GEN)>(p.plan, u0, u1, per, s_pref, VB, Hkv);
     }
   }
   tc_fence_before();
@@ -961,11 +963,16 @@ cudaError_t go(const uint8_t* kc, const uint8_t* vc, const Kv8AttnParams& p, int
   auto k = kv8_prefill_kernel<D, GEN>;
   constexpr uint32_t smem = prefill_smem(D).total;
   // the roles' register shares must fit what the launch has, or their exchange would not end
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, k);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> seen{0};
+  static std::atomic<int> regs{0};
+  cudaError_t e = cudaSuccess;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+  e = allow_smem(k, smem, seen);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(grid), dim3(kThreads), smem, s, kc, vc, p);
   if (e != cudaSuccess || grid == 1) return e;

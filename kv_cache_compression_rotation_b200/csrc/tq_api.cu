@@ -45,8 +45,15 @@ tq_status fail(tq_status s, const char* fmt, ...) {
 }
 
 int* device_status_ptr() {
+  // one address a device; asking the runtime costs a microsecond of every call
+  static std::atomic<int*> known[kKnownDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev < kKnownDevices)
+    if (int* ptr = known[dev].load(std::memory_order_relaxed)) return ptr;
   void* ptr = nullptr;
   if (cudaGetSymbolAddress(&ptr, g_tq_status) != cudaSuccess) return nullptr;
+  if (dev < kKnownDevices) known[dev].store(static_cast<int*>(ptr), std::memory_order_relaxed);
   return static_cast<int*>(ptr);
 }
 
@@ -70,9 +77,14 @@ bool overlaps(Range a, Range b) {
 }  // namespace
 
 int sm_count() {
+  static std::atomic<int> known[kKnownDevices];
   int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return n;
+  if (dev < kKnownDevices)
+    if (const int k = known[dev].load(std::memory_order_relaxed)) return k;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < kKnownDevices) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 namespace {

@@ -25,6 +25,8 @@ tq_status spectral_descriptor(const double* vecs, const double* vals, int d, int
 // The shape and descriptor checks tq_decode_attn runs before anything else (tq_api.cu).
 tq_status decode_shape_ok(const tq_quantizer* kq, const tq_quantizer* vq, int B, int Hq, int Hkv, int64_t Nmax);
 
+constexpr int kKnownDevices = 64;    // devices whose properties are kept between calls
+
 // Argument checks shared by the entry points (tq_api.cu).
 struct Range {
   const void* p;

@@ -7,6 +7,7 @@ fallback.  Build it with ``python -m kv_cache_compression_rotation_b200.build``.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -196,8 +197,11 @@ def _dptr(t) -> Optional[int]:
 
 def _stream(stream=None) -> int:
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t) -> int:
@@ -662,11 +666,12 @@ def _rows(t, name: str, d: int):
 
 def _same_device(device, *ts):
     import torch
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device} in one call")
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors must be on the current CUDA device (got {device})")
+    index = device.index
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {device} and {t.device} in one call")
 
 
 def _kv8_cache(kcache: Kv8, vcache: Kv8, B: int, Hkv: int, Nmax: int, pages):
@@ -704,8 +709,13 @@ def kv8_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, T: int, d: int, Nmax: 
     """Workspace of the 8-bit attention calls (T = 1: decode); dtype as a torch dtype."""
     import torch
     code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
+    return _kv8_ws_bytes(torch.cuda.current_device() if torch.cuda.is_initialized() else -1, code, B, Hq, Hkv, T, d, Nmax)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_ws_bytes(device: int, code: int, *shape) -> int:
     ws = C.c_size_t(0)
-    _check(lib().tq_kv8_attn_workspace(code, B, Hq, Hkv, T, d, Nmax, C.byref(ws)))
+    _check(lib().tq_kv8_attn_workspace(code, *shape, C.byref(ws)))
     return ws.value
 
 
@@ -803,6 +813,7 @@ class PagePool:
                 raise ValueError(f"array {i} must be contiguous, on {self.device}, and a whole number of bytes a page")
             pa[i] = PoolArray_t(a.data_ptr(), nbytes // self.num_pages)
         self.pa = pa
+        self.ws_bytes = {}                     # by number of requests
         self.c = PagePool_t(block_table.data_ptr(), refs.data_ptr(), self.rows, self.max_pages, page_size,
                             self.num_pages)
 
@@ -812,9 +823,12 @@ class PagePool:
 
     def _work(self, n: int):
         import torch
-        ws = C.c_size_t(0)
-        _check(lib().tq_pages_workspace(C.byref(self.c), n, C.byref(ws)))
-        return torch.empty(ws.value, dtype=torch.uint8, device=self.device)
+        size = self.ws_bytes.get(n)
+        if size is None:
+            ws = C.c_size_t(0)
+            _check(lib().tq_pages_workspace(C.byref(self.c), n, C.byref(ws)))
+            size = self.ws_bytes[n] = ws.value
+        return torch.empty(size, dtype=torch.uint8, device=self.device)
 
 
 def _one_int(pool: PagePool):
