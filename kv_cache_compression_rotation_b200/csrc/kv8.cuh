@@ -132,15 +132,15 @@ __device__ __forceinline__ void kv8_prefix(int* pref, int VB) {
 }
 
 // A CTA that starts inside a key head's units says so for the kernel that joins: plan[c] = {v, h, c0,
-// c1}, the CTAs that worked on it, if c is the second of them, else v = -1.  A key head has COST
+// c1}, the CTAs that worked on it, if c is the second of them, else v = -1.  A key head has `cost`
 // units before its tiles.
-template <int COST>
-__device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1, int64_t per, const int* pref, int VB, int Hkv) {
+__device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1, int64_t per, const int* pref, int VB, int Hkv,
+                                               int cost) {
   int4 s = make_int4(-1, 0, 0, 0);
   if (u0 < u1 && u0 > 0) {
     const Kv8Place p = kv8_place_of(u0, pref, VB, Hkv);
     const int64_t start = u0 - p.tile;
-    s.z = static_cast<int>((start + COST) / per);
+    s.z = static_cast<int>((start + cost) / per);
     s.w = static_cast<int>((start + p.n - 1) / per);
     if (p.tile > 0 && s.z + 1 == static_cast<int>(blockIdx.x)) {
       s.x = p.v;
@@ -150,8 +150,23 @@ __device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1
   reinterpret_cast<int4*>(plan)[blockIdx.x] = s;
 }
 
-// plan[]: tiles a CTA (64 bits), then pref, for the kernel that joins.
-constexpr int kKv8PlanHead = 2;
+// Tiles [tile, tile + tiles) of the n of key head h of virtual sequence v: what a CTA does from unit u
+// of the line to u1 or to the end of the key head, which has `cost` units before those of its tiles.
+struct Kv8Run {
+  int v, h, tile, tiles, n, units;
+};
+
+__device__ __forceinline__ Kv8Run kv8_run_at(int64_t u, int64_t u1, const int* pref, int VB, int Hkv, int cost) {
+  const Kv8Place p = kv8_place_of(u, pref, VB, Hkv);
+  Kv8Run r;
+  r.v = p.v;
+  r.h = p.h;
+  r.n = p.n - cost;
+  r.units = static_cast<int>(min(u1 - u, static_cast<int64_t>(p.n - p.tile)));
+  r.tile = max(0, p.tile - cost);
+  r.tiles = max(0, p.tile + r.units - cost) - r.tile;
+  return r;
+}
 
 // The NaN codes (0x7f, 0xff) of four bytes as 0.
 __device__ __forceinline__ uint32_t e4m3_nan_to_zero(uint32_t w) {

@@ -137,7 +137,7 @@ tq_status prepare_append(const Append& a, int dtype, int B, int Hkv, int d, cons
 struct AttnPlan {
   bool prefill;        // the tensor-memory kernel
   int64_t VB;          // virtual sequences: row groups of a sequence
-  int RG, grid, max_vb;
+  int RG, grid, max_vb, run_cost;
   size_t off_lse, off_plan, bytes;
 };
 
@@ -159,6 +159,9 @@ AttnPlan plan_attn(int dtype, int B, int Hkv, int G, int T, int d, int64_t cap) 
   // decode: eight tiles a CTA at least, one a warp
   const int64_t tiles = std::min<int64_t>(P.VB, P.max_vb) * Hkv * (cap / tile + 2), least = P.prefill ? 1 : 8;
   P.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (tiles + least - 1) / least)));
+  // A key head's run costs a decode CTA about 16 tiles beside its own (q, and the joining of the warps),
+  // but where a CTA gets few tiles the cut would be the cost's, not the tiles'.
+  P.run_cost = static_cast<int>(std::clamp<int64_t>((tiles / P.grid - 16) / 4, 0, 16));
   P.off_lse = static_cast<size_t>(2) * P.grid * rows * d * 4;
   P.off_plan = P.off_lse + up16(static_cast<size_t>(2) * P.grid * rows * 4);
   P.bytes = P.off_plan + up16((std::max(kKv8DecodeMaxVB, kKv8PrefillMaxVB) + 3) * 4);
@@ -282,6 +285,8 @@ tq_status run_attn(const AttnCall& c) {
   p.plan = reinterpret_cast<int*>(ws + P.off_plan);
   p.status = device_status_ptr();
   p.wait_limit = wait_limit();
+  p.appended = c.append != nullptr;
+  p.run_cost = P.run_cost;
   for (int64_t v = 0; v < P.VB; v += P.max_vb) {
     p.v0 = static_cast<int>(v);
     p.VB = static_cast<int>(std::min<int64_t>(P.max_vb, P.VB - v));

@@ -44,6 +44,35 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float r) {
   return to_e4m3x4(a.x * r, a.y * r, b.x * r, b.y * r);
 }
 
+// Eight neighbouring values of a row as they came: 16-bit types in one 16-byte word, fp32 in two.
+template <int DT>
+struct Eight {
+  uint4 w[DT == TQ_F32 ? 2 : 1];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (uint4& x : w) x = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+#pragma unroll
+    for (int i = 0; i < (DT == TQ_F32 ? 2 : 1); ++i)
+      w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (DT == TQ_F32 ? 4 : 2)) + i);
+  }
+  // Values 2 i, 2 i + 1.
+  __device__ __forceinline__ float2 at(int i) const {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    if constexpr (DT == TQ_F32) {
+      const uint32_t v[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+      return i < 2 ? make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))
+                   : make_float2(__uint_as_float(v[2 * i - 4]), __uint_as_float(v[2 * i - 3]));
+    } else if constexpr (DT == TQ_BF16) {
+      return make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    } else {
+      return __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    }
+  }
+};
+
 template <int D, int DT>
 __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8AppendParams p) {
   constexpr int LPR = D / 8;          // lanes a row
@@ -52,14 +81,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
+  // The warps of neighbouring heads stand together: a projection leaves a token's heads side by side.
   int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t per_side = static_cast<int64_t>(p.B) * p.map.Hkv * p.blocks;
-  const int side = w >= per_side ? 1 : 0;
-  w -= side * per_side;
-  if (w >= per_side) return;
+  const int h = static_cast<int>(w % p.map.Hkv);
+  w /= p.map.Hkv;
   const int j = static_cast<int>(w % p.blocks);
-  const int bh = static_cast<int>(w / p.blocks);
-  const int b = bh / p.map.Hkv, h = bh - b * p.map.Hkv;
+  w /= p.blocks;
+  const int b = static_cast<int>(w % p.B), side = static_cast<int>(w / p.B);
+  if (side > 1) return;
 
   const int len = __ldg(p.kv_lens + b);
   const int fresh = p.new_lens ? __ldg(p.new_lens + b) : p.T;
@@ -72,45 +101,35 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
   if (fresh == 0 || t0 >= len) return;
   const int held = max(0, p0 - t0), end = min(kKv8Block, len - t0);
 
-  const int64_t rec = kv8_record(p.map, b, h, t0, p.status);
-  uint8_t* codes = p.codes[side] + rec * D;
-  float* scale = p.scales[side] + rec / kKv8Block;
-
+  // the page's id and the rows are asked for together
+  const int page = static_cast<int>(p.map.page), pcol = t0 / page;
+  int64_t id = b;
+  if (p.map.table) id = __ldg(p.map.table + static_cast<int64_t>(b) * p.map.max_pages + pcol);
   const int row0 = lane / LPR, col = (lane % LPR) * 8;
   const int64_t base = b * p.stride_b[side] + h * p.stride_h[side] + col;
-  float v[NP][8];
-  float amax = 0.f;
+  Eight<DT> v[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int r = k * RPP + row0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-    if (r >= held && r < end) {
-      const int64_t at = base + static_cast<int64_t>(t0 + r - p0) * p.stride_t[side];
-      if constexpr (DT == TQ_F32) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.x[side]) + at);
-        const float4 a = __ldg(s), c = __ldg(s + 1);
-        v[k][0] = a.x; v[k][1] = a.y; v[k][2] = a.z; v[k][3] = a.w;
-        v[k][4] = c.x; v[k][5] = c.y; v[k][6] = c.z; v[k][7] = c.w;
-      } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[side]) + at));
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (DT == TQ_BF16) {
-            v[k][2 * i] = __uint_as_float(u[i] << 16);
-            v[k][2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-          } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            v[k][2 * i] = f.x;
-            v[k][2 * i + 1] = f.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[k][i]));
-    }
+    v[k].clear();
+    if (r >= held && r < end) v[k].load(p.x[side], base + static_cast<int64_t>(t0 + r - p0) * p.stride_t[side]);
   }
+  if (id < 0 || id >= p.map.num_pages) {
+    report_status(p.status, TQ_ERR_INVALID_ARG);
+    id = 0;
+  }
+  const int64_t rec = (id * p.map.Hkv + h) * p.map.page + (t0 - pcol * page);
+  uint8_t* codes = p.codes[side] + rec * D;
+  float* scale = p.scales[side] + rec / kKv8Block;
+
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = v[k].at(i);
+      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
   const int need = scale_exponent(warp_max(amax));
   int e = need;
   if (held) {
@@ -119,14 +138,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
     if (need > old) {
       // 2^(old - need); below 2^-126 every held code rounds to 0 either way
       const float r = __uint_as_float(static_cast<uint32_t>(max(127 + old - need, 0)) << 23);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int row = k * RPP + row0;
-        if (row < held) {
-          uint2* c = reinterpret_cast<uint2*>(codes + row * D + col);
-          const uint2 w2 = *c;
-          *c = make_uint2(rescale_e4m3x4(w2.x, r), rescale_e4m3x4(w2.y, r));
-        }
+#pragma unroll 1
+      for (int row = row0; row < held; row += RPP) {
+        uint2* c = reinterpret_cast<uint2*>(codes + row * D + col);
+        const uint2 w2 = *c;
+        *c = make_uint2(rescale_e4m3x4(w2.x, r), rescale_e4m3x4(w2.y, r));
       }
     }
   }
@@ -136,10 +152,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int r = k * RPP + row0;
-    if (r >= held && r < end)
-      *reinterpret_cast<uint2*>(codes + r * D + col) =
-          make_uint2(to_e4m3x4(v[k][0] * inv, v[k][1] * inv, v[k][2] * inv, v[k][3] * inv),
-                     to_e4m3x4(v[k][4] * inv, v[k][5] * inv, v[k][6] * inv, v[k][7] * inv));
+    if (r >= held && r < end) {
+      const float2 f0 = v[k].at(0), f1 = v[k].at(1), f2 = v[k].at(2), f3 = v[k].at(3);
+      *reinterpret_cast<uint2*>(codes + r * D + col) = make_uint2(to_e4m3x4(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
+                                                                  to_e4m3x4(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
+    }
   }
   if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(e) << 23);
 }

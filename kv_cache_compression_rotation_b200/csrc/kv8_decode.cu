@@ -33,22 +33,28 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTile = 32;                  // tokens
-constexpr int kMinTiles = kWarps;          // a CTA's run, where there is little work
+constexpr int kMinTiles = kWarps;          // a CTA's tiles, where there is little work
+// Outputs of 8 * NT rows on their way to the sum over the warps: a lane of the product holds two
+// neighbouring dims of row 2 (lane % 4) + c and eighth lane / 4 of the dims; the padding keeps the
+// lanes' banks apart.
+__host__ __device__ constexpr int eighth(int D) { return D / 8 + 2; }
+__host__ __device__ constexpr int out_stride(int D) { return 8 * eighth(D) + 4; }
 
 __host__ __device__ constexpr int ring_stages(int D, int NT) { return D == 64 ? 4 : (NT == 1 ? 3 : 2); }
 __host__ __device__ constexpr uint32_t stage_bytes(int D) { return 2u * kTile * D; }
 
 struct DecodeSmem {
-  uint32_t scales, bars, lo, hi, pref, ml, o, total;
+  uint32_t scales, bars, lo, hi, pref, ml, fin, o, total;
 };
 __host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT) {
   const int ns = ring_stages(D, NT);
   DecodeSmem L{};
   uint32_t at = kWarps * ns * stage_bytes(D);
-  L.o = at; at += 4u * 8 * NT * D * 4;                         // four warps' outputs
+  L.o = at; at += 4u * 8 * NT * out_stride(D) * 4;             // four warps' outputs
   L.scales = at; at += kWarps * ns * 16;
   L.bars = at; at += kWarps * ns * 8;
   L.ml = at; at += kWarps * (16 * 2 + 1) * 4;                  // m, l of 16 rows and E
+  L.fin = at; at += 16 * 2 * 4;                                // 1 / sum and lse of 16 rows
   L.lo = at; at += kKv8DecodeMaxVB * 4;
   L.hi = at; at += kKv8DecodeMaxVB * 4;
   L.pref = at; at += (kKv8DecodeMaxVB + 1) * 4;
@@ -93,6 +99,20 @@ __device__ __forceinline__ uint32_t swz(int r, uint32_t off) {
   return D == 128 ? r * 128u + (off ^ ((r & 7u) << 4)) : r * 64u + (off ^ (((r >> 1) & 3u) << 4));
 }
 
+// Four outputs at element `at`; W == 2: fp32.
+template <int W>
+__device__ __forceinline__ void store4(void* out, int dtype, int64_t at, float2 x, float2 y) {
+  if (W == 2) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(x.x, x.y, y.x, y.y);
+  } else if (dtype == TQ_BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(y.x, y.y);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_h2(x.x, x.y), pack_h2(y.x, y.y));
+  }
+}
+
 template <int D, int NT, int W>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -111,6 +131,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   int* s_pref = reinterpret_cast<int*>(sm + L.pref);
   float* s_ml = reinterpret_cast<float*>(sm + L.ml);
   float* s_o = reinterpret_cast<float*>(sm + L.o);
+  float* s_fin = reinterpret_cast<float*>(sm + L.fin);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.total - 1024 - 16);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -118,13 +139,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   const uint32_t ring = base + warp * NS * SB;
   const uint32_t bar0 = base + L.bars + warp * NS * 8;
   const uint32_t sc0 = base + L.scales + warp * NS * 16;
+  const int ppb = static_cast<int>(p.map.page / kKv8Block);
   if (lane == 0)
     for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 5);
   if (tid == 0) {
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_wait();
+  if (!p.appended) pdl_wait();               // (behind an append nothing that it writes is read before the second wait)
 
   // ---- how the work is cut
   const int VB = p.VB, Hkv = p.map.Hkv, R = p.T * p.G;
@@ -140,35 +162,48 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     s_lo[v] = hi > 0 ? lo : 0;
     s_hi[v] = hi;
-    s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
+    s_pref[v + 1] = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile + p.run_cost : 0;
   }
   __syncthreads();
   if (warp == 0) kv8_prefix(s_pref, VB);
   __syncthreads();
   const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
   const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinTiles));
-  if (blockIdx.x == 0) {
-    for (int v = tid; v <= VB; v += kWarps * 32) p.plan[kKv8PlanHead + v] = s_pref[v];
-    if (tid == 0) *reinterpret_cast<int64_t*>(p.plan) = per;
-  }
-  pdl_trigger();
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
+  if (p.appended) pdl_wait();
+  pdl_trigger();
 
-  // ---- issue side: this warp's tiles u0 + warp, + kWarps, ...
-  int64_t iu = u0 + warp;
-  Kv8Place ip{};
-  if (iu < u1) ip = kv8_place_of(iu, s_pref, VB, Hkv);
-  int issued = 0, used = 0;
+  // ---- issue side: every eighth tile of the CTA's runs
+  int64_t iu = u0;
+  Kv8Run ir{};
+  int ij = warp, issued = 0, used = 0, id = 0, place = 0;
+  // Moves to the run of the warp's next tile and asks for the page of its block lane % 2.
+  auto ask = [&]() {
+    while (ij >= ir.tiles) {
+      ij -= ir.tiles;
+      iu += ir.units;
+      if (iu >= u1) return;
+      ir = kv8_run_at(iu, u1, s_pref, VB, Hkv, p.run_cost);
+    }
+    if (lane < 4) {
+      // a block outside the visible tokens may have no page: the nearest visible one instead
+      const int lo = s_lo[ir.v], hi = s_hi[ir.v], b = (p.v0 + ir.v) / p.RG;
+      const int blk = min(max((lo / kTile + ir.tile + ij) * 2 + (lane & 1), lo / kKv8Block), (hi - 1) / kKv8Block);
+      const int col = blk / ppb;
+      place = blk - col * ppb;
+      id = p.map.table ? __ldg(p.map.table + static_cast<int64_t>(b) * p.map.max_pages + col) : b;
+    }
+  };
   auto issue = [&]() {
     if (iu >= u1) return;
     const int st = issued % NS;
     const uint32_t bar = bar0 + 8 * st, dst = ring + st * SB;
     if (lane < 4) {
-      const int b = (p.v0 + ip.v) / p.RG;
-      // a block outside the visible tokens may have no page: the nearest visible one instead
-      const int lo = s_lo[ip.v], hi = s_hi[ip.v];
-      const int blk = min(max((lo / kTile + ip.tile) * 2 + (lane & 1), lo / kKv8Block), (hi - 1) / kKv8Block);
-      const int64_t rec = kv8_record(p.map, b, ip.h, static_cast<int64_t>(blk) * kKv8Block, p.status);
+      if (id < 0 || id >= p.map.num_pages) {
+        report_status(p.status, TQ_ERR_INVALID_ARG);
+        id = 0;
+      }
+      const int64_t rec = (static_cast<int64_t>(id) * Hkv + ir.h) * p.map.page + place * kKv8Block;
       if (lane == 0) mbar_expect_tx(bar, SB);
       __syncwarp(0xfu);
       if (lane < 2) {
@@ -184,24 +219,19 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     __syncwarp();
     ++issued;
-    iu += kWarps;
-    ip.tile += kWarps;
-    while (ip.tile >= ip.n && iu < u1) {
-      ip.tile -= ip.n;
-      if (++ip.h == Hkv) {
-        ip.h = 0;
-        do { ++ip.v; ip.n = s_pref[ip.v + 1] - s_pref[ip.v]; } while (ip.n == 0);
-      }
-    }
+    ij += kWarps;
+    ask();
   };
+  ask();
   for (int s = 0; s < NS; ++s) issue();
 
   // ---- consume side, one (sequence, key head) at a time
-  int64_t cu = u0 + warp;
+  int cj = warp;
   bool dead = false;
   for (int64_t u = u0; u < u1;) {
-    const Kv8Place sp = kv8_place_of(u, s_pref, VB, Hkv);
-    const int64_t seg_end = min(u1, u + sp.n - sp.tile);
+    const Kv8Run sp = kv8_run_at(u, u1, s_pref, VB, Hkv, p.run_cost);
+    u += sp.units;
+    if (sp.tiles == 0) continue;
     const int gv = p.v0 + sp.v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
     const int len = kv8_len(p.sc.kv_lens, b, p.map.cap, nullptr);
 
@@ -293,14 +323,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.f;
     int E = 1;                                   // largest value-scale exponent so far (biased)
 
-    for (; cu < seg_end; cu += kWarps) {
+    for (; cj < sp.tiles; cj += kWarps) {
       const int st = used % NS;
       const uint32_t bar = bar0 + 8 * st, ks_a = ring + st * SB, vs_a = ks_a + kTile * D;
       if (!dead && !mbar_wait(bar, (used / NS) & 1, p.wait_limit, p.status, abort_flag)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       if (dead) continue;
       ++used;
-      const int t0 = (s_lo[sp.v] / kTile + sp.tile + static_cast<int>(cu - u)) * kTile;
+      const int t0 = (s_lo[sp.v] / kTile + sp.tile + cj) * kTile;
       const bool masked = t0 < in_lo || t0 + kTile > in_hi;
       float4 sc;                                 // key scales, value scales of the two blocks
       asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(sc.x), "=f"(sc.y), "=f"(sc.z), "=f"(sc.w)
@@ -447,6 +477,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       issue();                                  // into the stage just read
     }
 
+    cj -= sp.tiles;
     // ---- join the warps: common maximum and value scale, then sums in a fixed order
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -464,7 +495,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     float Em = 1.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) Em = fmaxf(Em, s_ml[w * 33 + 32]);
-    float M[NT][2], Ls[NT][2];
+    const float unit = __uint_as_float(static_cast<uint32_t>(Em) << 23);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -476,8 +507,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) ll += s_ml[w * 33 + 16 + r] * ex2(s_ml[w * 33 + r] - ref);
-        M[nt][c] = mm;
-        Ls[nt][c] = ll;
+        if (warp == 0 && g == 0) {
+          s_fin[2 * r] = ll == 0.f ? 0.f : 1.f / (ll * 32768.f);
+          s_fin[2 * r + 1] = ll == 0.f ? -INFINITY : mm + __log2f(ll);
+        }
         const float a = ex2(m[nt][c] - ref + (static_cast<float>(E) - Em));
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -485,72 +518,68 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           acc[i][nt][2 + c] *= a;
         }
       }
+    // Warps 4..7 leave their outputs, warps 0..3 add theirs to them; then every thread sums four.
+    constexpr int RS = out_stride(D);
 #pragma unroll
-    for (int half = kWarps / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-        float* o = s_o + (warp - half) * 8 * NT * D;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * D + (D / 8) * g + 2 * i) =
-                  make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
-      }
-      __syncthreads();
-      if (warp < half) {
-        const float* o = s_o + warp * 8 * NT * D;
+    for (int half = 1; half >= 0; --half) {
+      if (warp / 4 == half) {
+        float* o = s_o + (warp & 3) * 8 * NT * RS + eighth(D) * g;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float2 x = *reinterpret_cast<const float2*>(o + (nt * 8 + 2 * qd + c) * D + (D / 8) * g + 2 * i);
-              acc[i][nt][c] += x.x;
-              acc[i][nt][2 + c] += x.y;
+              float2* at = reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * RS + 2 * i);
+              float2 x = make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
+              if (half == 0) {
+                x.x += at->x;
+                x.y += at->y;
+              }
+              *at = x;
             }
       }
       __syncthreads();
     }
-    if (warp == 0) {
-      const bool whole = sp.tile == 0 && seg_end - u == sp.n;
+    const bool whole = sp.tiles == sp.n;
+    const int slot = blockIdx.x * 2 + (sp.tile == 0 ? 1 : 0);
+    for (int e = tid; e < 8 * NT * (D / 4); e += kWarps * 32) {
+      const int rl = e / (D / 4), col = (e - rl * (D / 4)) * 4, r = r0 + rl;
+      if (r >= R) break;
+      const float* o = s_o + rl * RS + eighth(D) * (col / (D / 8)) + col % (D / 8);
+      float2 x = make_float2(0.f, 0.f), y = x;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 a = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS);
+        const float2 c = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS + 2);
+        x.x += a.x; x.y += a.y; y.x += c.x; y.y += c.y;
+      }
       // the sums are in units of 2^(Em - 127 - 15); two factors, so that neither leaves the normal range
-      const float unit = __uint_as_float(static_cast<uint32_t>(Em) << 23);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rl = nt * 8 + 2 * qd + c, r = r0 + rl;
-          const float inv = Ls[nt][c] == 0.f ? 0.f : 1.f / (Ls[nt][c] * 32768.f);
-          const float ls2 = Ls[nt][c] == 0.f ? -INFINITY : M[nt][c] + __log2f(Ls[nt][c]);
-          if (whole) {
-            if (r < R) {
-              const int i = r / p.G;
-              const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
-              if (p.lse && g == 0) p.lse[row] = ls2 * kLn2;
-#pragma unroll
-              for (int k = 0; k < MT; ++k) {
-                const float x = acc[k][nt][c] * inv * unit, y = acc[k][nt][2 + c] * inv * unit;
-                const int64_t at = row * D + (D / 8) * g + 2 * k;
-                if (W == 2) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
-                else if (p.dtype == TQ_BF16)
-                  *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + at) = __floats2bfloat162_rn(x, y);
-                else *reinterpret_cast<__half2*>(static_cast<__half*>(p.out) + at) = __floats2half2_rn(x, y);
-              }
-            }
-          } else {
-            const int slot = blockIdx.x * 2 + (sp.tile == 0 ? 1 : 0);
-            if (g == 0) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
-            float* o = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + (D / 8) * g;
-#pragma unroll
-            for (int k = 0; k < MT; ++k)
-              *reinterpret_cast<float2*>(o + 2 * k) = make_float2(acc[k][nt][c] * inv * unit, acc[k][nt][2 + c] * inv * unit);
-          }
-        }
+      const float inv = s_fin[2 * rl], ls2 = s_fin[2 * rl + 1];
+      x.x = x.x * inv * unit; x.y = x.y * inv * unit; y.x = y.x * inv * unit; y.y = y.y * inv * unit;
+      if (whole) {
+        const int i = r / p.G;
+        const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
+        if (p.lse && col == 0) p.lse[row] = ls2 * kLn2;
+        store4<W>(p.out, p.dtype, row * D + col, x, y);
+      } else {
+        if (col == 0) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
+        *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + col) =
+            make_float4(x.x, x.y, y.x, y.y);
+      }
     }
-    u = seg_end;
+  }
+  if (blockIdx.x > 0 && tid == 0) kv8_plan_split(p.plan, u0, u1, per, s_pref, VB, Hkv, p.run_cost);
+  // ---- groups that see nothing
+  for (int v = blockIdx.x; v < VB; v += gridDim.x) {
+    if (s_pref[v + 1] != s_pref[v]) continue;
+    const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows, n = min(R - r0, kKv8DecodeRows);
+    for (int e = tid; e < Hkv * n * (D / 4); e += kWarps * 32) {
+      const int hr = e / (D / 4), h = hr / n, r = r0 + hr - h * n, i = r / p.G, col = (e - hr * (D / 4)) * 4;
+      const int64_t row = (static_cast<int64_t>(b) * p.Hq + h * p.G + (r - i * p.G)) * p.T + i;
+      if (p.lse && col == 0) p.lse[row] = -INFINITY;
+      store4<W>(p.out, p.dtype, row * D + col, make_float2(0.f, 0.f), make_float2(0.f, 0.f));
+    }
   }
   // copies still in flight land before the CTA ends (none, unless a wait gave up)
   for (; used < issued; ++used)
@@ -558,41 +587,37 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 }
 
 // Joins the partial results of a (virtual sequence, key head) that several CTAs worked on:
-// out = sum_c w_c out_c / sum_c w_c, w_c = 2^(lse_c - max).  One block a pair; a pair with no
-// visible token gets zeros.
+// out = sum_c w_c out_c / sum_c w_c, w_c = 2^(lse_c - max).  Blocks: the CTAs' boundaries.
 template <int D>
-__global__ void __launch_bounds__(128) kv8_decode_join_kernel(const Kv8AttnParams p) {
+__global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Kv8AttnParams p) {
   pdl_wait();
   pdl_trigger();
-  const int Hkv = p.map.Hkv, v = blockIdx.x / Hkv, h = blockIdx.x - v * Hkv;
-  const int64_t per = __ldg(reinterpret_cast<const int64_t*>(p.plan));
-  const int t0 = __ldg(p.plan + kKv8PlanHead + v), n = __ldg(p.plan + kKv8PlanHead + v + 1) - t0;
-  const int64_t u = static_cast<int64_t>(t0) * Hkv + static_cast<int64_t>(h) * n;
-  const int c0 = static_cast<int>(u / per), c1 = n ? static_cast<int>((u + n - 1) / per) : c0;
-  if (n && c0 == c1) return;                   // finished where it was computed
-  const int gv = p.v0 + v, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
+  const int4 split = __ldcg(reinterpret_cast<const int4*>(p.plan) + blockIdx.x + 1);
+  if (split.x < 0) return;
+  const int h = split.y, c0 = split.z, c1 = split.w;
+  const int gv = p.v0 + split.x, b = gv / p.RG, r0 = (gv - b * p.RG) * kKv8DecodeRows;
   const int R = p.T * p.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int PL = D / 32;                   // dims a lane
-  for (int rl = warp; rl < kKv8DecodeRows && r0 + rl < R; rl += 4) {
+  for (int rl = warp; rl < kKv8DecodeRows && r0 + rl < R; rl += 8) {
     const int r = r0 + rl, i = r / p.G;
     const int64_t row = (static_cast<int64_t>(b) * p.Hq + h * p.G + (r - i * p.G)) * p.T + i;
     float mx = -INFINITY, sum = 0.f, o[PL];
 #pragma unroll
     for (int k = 0; k < PL; ++k) o[k] = 0.f;
     auto slot_of = [&](int c) { return c * 2 + (c == c0 ? 1 : 0); };
-    if (n) {
-      for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldg(p.part_lse + slot_of(c) * kKv8DecodeRows + rl));
-      mx = warp_max(mx);
-      if (mx > -INFINITY)
-        for (int c = c0; c <= c1; ++c) {
-          const int slot = slot_of(c);
-          const float w = ex2(__ldg(p.part_lse + slot * kKv8DecodeRows + rl) - mx);
-          sum += w;
-          const float* src = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + lane * PL;
+    for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.part_lse + slot_of(c) * kKv8DecodeRows + rl));
+    mx = warp_max(mx);
+    if (mx > -INFINITY) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const int slot = slot_of(c);
+        const float w = ex2(__ldcg(p.part_lse + slot * kKv8DecodeRows + rl) - mx);
+        sum += w;
+        const float* src = p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + lane * PL;
 #pragma unroll
-          for (int k = 0; k < PL; ++k) o[k] += w * __ldg(src + k);
-        }
+        for (int k = 0; k < PL; ++k) o[k] += w * __ldcg(src + k);
+      }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
@@ -615,8 +640,8 @@ cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams
   cudaError_t e = allow_smem(k, smem, seen);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(grid), dim3(kWarps * 32), smem, s, km, vm, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_decode_join_kernel<D>, dim3(static_cast<unsigned>(p.VB) * p.map.Hkv), dim3(128), 0, s, p);
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_pdl(kv8_decode_join_kernel<D>, dim3(grid - 1), dim3(256), 0, s, p);
 }
 
 template <int D>

@@ -52,9 +52,11 @@ struct Kv8AttnParams {
   float* lse;                                         // [B][Hq][T] or nullptr
   float* part_o;                                      // partial results of split rows
   float* part_lse;
-  int* plan;                                          // how the launch's work is split
+  int* plan;                                          // where the launch's work is split
   int* status;
   long long wait_limit;
+  int run_cost;                                       // decode: see plan_attn
+  bool appended;                                      // behind an append of the same call
 };
 // Groups of 16 rows a key head (decode; fp32 queries).  kmap / vmap: the codes as [records][d]
 // bytes in boxes of 16 rows.

@@ -47,10 +47,9 @@ constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsRest = 48, kRegsLaunch
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
 constexpr int kScouts = 32;                  // the warp that prepares runs
 
-// A run: tiles [tile, tile + tiles) of the n of key head h of virtual sequence v, which is rows r0 ..
-// of sequence b; tile 0 of the run starts at token t0.  tiles = 0: no more.
-struct Run {
-  int v, h, tile, tiles, n, units, b, r0, t0;
+// A run, on rows r0 .. of sequence b; its first tile starts at token t0.  tiles = 0: no more.
+struct Run : Kv8Run {
+  int b, r0, t0;
   int lo, hi;                                // tokens that some row sees
   int in_lo, in_hi;                          // tokens that all rows see
 };
@@ -216,21 +215,6 @@ __device__ __forceinline__ void tanh_small(float (&s)[32], int at, float in, flo
     s[at + 2 * k] = y.x;
     s[at + 2 * k + 1] = y.y;
   }
-}
-
-// The run that starts at unit u of the line and ends at u1 or with its key head.  A key head takes
-// `cost` units and one for each tile.
-__device__ __forceinline__ Run run_at(int64_t u, int64_t u1, const int* pref, int VB, int Hkv, int cost) {
-  const Kv8Place p = kv8_place_of(u, pref, VB, Hkv);
-  Run r;
-  r.v = p.v;
-  r.h = p.h;
-  r.n = p.n - cost;
-  r.units = static_cast<int>(min(u1 - u, static_cast<int64_t>(p.n - p.tile)));
-  r.tile = max(0, p.tile - cost);
-  r.tiles = max(0, p.tile + r.units - cost) - r.tile;
-  r.b = r.r0 = r.t0 = r.lo = r.hi = r.in_lo = r.in_hi = 0;
-  return r;
 }
 
 // GEN: scores are capped or biased.
@@ -867,7 +851,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         Run run{};
         int len = 0;
         if (u < u1) {
-          run = run_at(u, u1, s_pref, VB, Hkv, run_cost(GEN));
+          static_cast<Kv8Run&>(run) = kv8_run_at(u, u1, s_pref, VB, Hkv, run_cost(GEN));
           u += run.units;
           if (run.tiles == 0) continue;
           const int gv = p.v0 + run.v;
@@ -906,7 +890,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         mbar_arrive(bar(DFULL + mb));
         if (run.tiles == 0) break;
       }
-      if (lane == 0) kv8_plan_split<run_cost(GEN)>(p.plan, u0, u1, per, s_pref, VB, Hkv);
+      if (lane == 0) kv8_plan_split(p.plan, u0, u1, per, s_pref, VB, Hkv, run_cost(GEN));
     }
   }
   tc_fence_before();
