@@ -9,9 +9,9 @@
 // sequences load every SM alike.  A pair that one run covers is finished in the CTA; the others
 // leave at most two partial results a CTA, joined by a second, small kernel.
 //
-// Inside a CTA eight warps work without meeting: each keeps its own ring of tiles, copied by the
+// Inside a CTA the warps work without meeting: each keeps its own ring of tiles, copied by the
 // tensor-map engine into swizzled rows (the swizzle frees the reads of the value operand from
-// bank conflicts) and takes every eighth tile.  A tile's scores are S^T = K Q^T with 16 tokens as
+// bank conflicts) and takes every eighth or twelfth tile.  A tile's scores are S^T = K Q^T with 16 tokens as
 // the rows of an m16n8k16 product and eight query rows as its columns, so small groups of query
 // heads waste little of it; then O^T += V^T P^T with the dims as rows.  Codes become halves
 // (exact) on the way into the registers.  The order of the 16 dims of a step is free, as long as
@@ -31,23 +31,24 @@
 namespace tq {
 namespace {
 
-constexpr int kWarps = 8;
+// Warps of a CTA.  Their instructions' latency bounds a tile, so as many as the registers allow.
+__host__ __device__ constexpr int warps_of(int NT, int W) { return NT == 1 && W == 1 ? 12 : 8; }
 constexpr int kTile = 32;                  // tokens
-constexpr int kMinTiles = kWarps;          // a CTA's tiles, where there is little work
+constexpr int kMinTiles = 8;               // a CTA's tiles, where there is little work
 // Outputs of 8 * NT rows on their way to the sum over the warps: a lane of the product holds two
 // neighbouring dims of row 2 (lane % 4) + c and eighth lane / 4 of the dims; the padding keeps the
 // lanes' banks apart.
 __host__ __device__ constexpr int eighth(int D) { return D / 8 + 2; }
 __host__ __device__ constexpr int out_stride(int D) { return 8 * eighth(D) + 4; }
 
-__host__ __device__ constexpr int ring_stages(int D, int NT) { return D == 64 ? 4 : (NT == 1 ? 3 : 2); }
+__host__ __device__ constexpr int ring_stages(int D, int NT, int W) { return D == 64 ? 4 : (NT == 1 && W == 2 ? 3 : 2); }
 __host__ __device__ constexpr uint32_t stage_bytes(int D) { return 2u * kTile * D; }
 
 struct DecodeSmem {
   uint32_t scales, bars, lo, hi, pref, ml, fin, o, total;
 };
-__host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT) {
-  const int ns = ring_stages(D, NT);
+__host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT, int W) {
+  const int ns = ring_stages(D, NT, W), kWarps = warps_of(NT, W);
   DecodeSmem L{};
   uint32_t at = kWarps * ns * stage_bytes(D);
   L.o = at; at += 4u * 8 * NT * out_stride(D) * 4;             // four warps' outputs
@@ -61,7 +62,8 @@ __host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT) {
   L.total = at + 16 + 1024;                                    // abort flag, alignment
   return L;
 }
-static_assert(decode_smem(128, 1).total <= 232448 && decode_smem(128, 2).total <= 232448, "shared memory");
+static_assert(decode_smem(128, 1, 1).total <= 232448 && decode_smem(128, 1, 2).total <= 232448 &&
+              decode_smem(128, 2, 1).total <= 232448 && decode_smem(64, 1, 1).total <= 232448, "shared memory");
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -114,12 +116,12 @@ __device__ __forceinline__ void store4(void* out, int dtype, int64_t at, float2 
 }
 
 template <int D, int NT, int W>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(warps_of(NT, W) * 32, 1)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const Kv8AttnParams p) {
-  constexpr int NS = ring_stages(D, NT);
+  constexpr int NS = ring_stages(D, NT, W), kWarps = warps_of(NT, W);
   constexpr uint32_t SB = stage_bytes(D);
-  constexpr DecodeSmem L = decode_smem(D, NT);
+  constexpr DecodeSmem L = decode_smem(D, NT, W);
   constexpr int KJ = D / 64;               // 64-dim halves of a row
   constexpr int MT = D / 16;               // 16-dim rows of the output product
   extern __shared__ unsigned char dsm_raw[];
@@ -173,7 +175,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   if (p.appended) pdl_wait();
   pdl_trigger();
 
-  // ---- issue side: every eighth tile of the CTA's runs
+  // ---- issue side: the warp's share of the tiles of the CTA's runs
   int64_t iu = u0;
   Kv8Run ir{};
   int ij = warp, issued = 0, used = 0, id = 0, place = 0;
@@ -518,11 +520,12 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           acc[i][nt][2 + c] *= a;
         }
       }
-    // Warps 4..7 leave their outputs, warps 0..3 add theirs to them; then every thread sums four.
+    // The last four warps leave their outputs, four by four the others add theirs to them; then every
+    // thread sums four.
     constexpr int RS = out_stride(D);
 #pragma unroll
-    for (int half = 1; half >= 0; --half) {
-      if (warp / 4 == half) {
+    for (int four = kWarps / 4 - 1; four >= 0; --four) {
+      if (warp / 4 == four) {
         float* o = s_o + (warp & 3) * 8 * NT * RS + eighth(D) * g;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -532,7 +535,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             for (int c = 0; c < 2; ++c) {
               float2* at = reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * RS + 2 * i);
               float2 x = make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
-              if (half == 0) {
+              if (four < kWarps / 4 - 1) {
                 x.x += at->x;
                 x.y += at->y;
               }
@@ -635,11 +638,11 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Kv8AttnParam
 template <int D, int NT, int W>
 cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
   auto k = kv8_decode_kernel<D, NT, W>;
-  constexpr uint32_t smem = decode_smem(D, NT).total;
+  constexpr uint32_t smem = decode_smem(D, NT, W).total;
   static std::atomic<uint64_t> seen{0};
   cudaError_t e = allow_smem(k, smem, seen);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(grid), dim3(kWarps * 32), smem, s, km, vm, p);
+  e = launch_pdl(k, dim3(grid), dim3(warps_of(NT, W) * 32), smem, s, km, vm, p);
   if (e != cudaSuccess || grid == 1) return e;
   return launch_pdl(kv8_decode_join_kernel<D>, dim3(grid - 1), dim3(256), 0, s, p);
 }
