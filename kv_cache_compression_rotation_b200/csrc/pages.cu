@@ -9,7 +9,8 @@
 //
 // The bookkeeping reads 4 bytes a page and is bound by launch and memory latency; the copies are
 // bound by bytes, 2 a byte moved, and go in slices of 16 KB with four 16-byte loads in flight a
-// thread.
+// thread.  Pools of up to 16384 pages take one block of 1024 threads, which holds all counts in its
+// registers and the requests in shared memory, in place of the counting and the assigning kernel.
 #include "pages.h"
 
 #include <algorithm>
@@ -22,8 +23,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = kPageChunk / kThreads;  // counts a thread
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallPages = kSmallThreads * kPer, kSmallRequests = 2048, kSmallRows = 16384;
 
 // Sum over the block; every thread gets it.
+template <int N = kThreads>
 __device__ __forceinline__ int block_sum(int x, int* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -33,7 +37,7 @@ __device__ __forceinline__ int block_sum(int x, int* sh) {
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
+  for (int w = 0; w < N / 32; ++w) t += sh[w];
   return t;
 }
 
@@ -83,11 +87,28 @@ __device__ __forceinline__ bool mark(uint32_t* m, int r) {
   return atomicOr(m + (r >> 5), bit) & bit;
 }
 
+// Request i: its row, what it wants of it, and whether it is in range.
+template <bool FORK>
+__device__ __forceinline__ bool request(const PagesParams& p, int i, int& row, int& src, int& want) {
+  const int cap = p.pool.max_pages * p.pool.page_size, len = p.lens[i];
+  row = p.rows[i];
+  want = src = 0;
+  if (row < 0 || row >= p.pool.rows || len < 0 || len > cap) return false;
+  if (FORK) {
+    src = p.src[i];
+    want = len % p.pool.page_size ? 1 : 0;
+    return src >= 0 && src < p.pool.rows;
+  }
+  const int old = p.old_lens[i];
+  want = max(0, pages_of(len, p.pool.page_size) - pages_of(old, p.pool.page_size));
+  return old >= 0 && old <= cap;
+}
+
 // The last block: what the requests want, and whether they can be served at all.
 template <bool FORK>
 __device__ void scan_requests(const PagesParams& p, int* sh) {
   __shared__ int bad;
-  const int words = (p.pool.rows + 31) / 32, cap = p.pool.max_pages * p.pool.page_size;
+  const int words = (p.pool.rows + 31) / 32;
   if (threadIdx.x == 0) bad = 0;
   for (int i = threadIdx.x; i < 2 * words; i += kThreads) p.marks[i] = 0;
   __syncthreads();
@@ -96,20 +117,10 @@ __device__ void scan_requests(const PagesParams& p, int* sh) {
     const int i = i0 + threadIdx.x;
     int want = 0;
     if (i < p.n) {
-      const int row = p.rows[i], len = p.lens[i];
-      bool ok = row >= 0 && row < p.pool.rows && len >= 0 && len <= cap;
-      if (FORK) {
-        const int src = p.src[i];
-        ok = ok && src >= 0 && src < p.pool.rows;
-        if (ok) {
-          mark(p.marks + words, src);
-          want = len % p.pool.page_size ? 1 : 0;
-        }
-      } else {
-        const int old = p.old_lens[i];
-        ok = ok && old >= 0 && old <= cap;
-        if (ok) want = max(0, pages_of(len, p.pool.page_size) - pages_of(old, p.pool.page_size));
-      }
+      int row, src;
+      const bool ok = request<FORK>(p, i, row, src, want);
+      if (!ok) want = 0;
+      if (FORK && ok) mark(p.marks + words, src);
       if (!ok || mark(p.marks, row)) atomicOr(&bad, 1);
     }
     const int before = block_before(want, sh);
@@ -153,6 +164,106 @@ __device__ __forceinline__ void chunk_sums(const PagesParams& p, int chunk, int*
   all = block_sum(a, sh);
 }
 
+// Request i of a fork: its row shares the parent's whole pages (one block).
+__device__ __forceinline__ void share_pages(const PagesParams& p, int i) {
+  const tq_page_pool& pool = p.pool;
+  const int full = p.lens[i] / pool.page_size;
+  const int32_t* from = pool.block_table + static_cast<int64_t>(p.src[i]) * pool.max_pages;
+  int32_t* to = pool.block_table + static_cast<int64_t>(p.rows[i]) * pool.max_pages;
+  for (int c = threadIdx.x; c < full; c += kThreads) {
+    const int id = from[c];
+    to[c] = id;
+    if (id >= 0 && id < pool.num_pages) atomicAdd(pool.refs + id, 1);
+    else report_status(p.status, TQ_ERR_INVALID_ARG);
+  }
+}
+
+// The page that request i of a fork copies (-1: none).
+__device__ __forceinline__ int tail_page(const PagesParams& p, int i) {
+  const tq_page_pool& pool = p.pool;
+  const int len = p.lens[i];
+  if (len % pool.page_size == 0) return -1;
+  const int id = pool.block_table[static_cast<int64_t>(p.src[i]) * pool.max_pages + len / pool.page_size];
+  if (id >= 0 && id < pool.num_pages) return id;
+  report_status(p.status, TQ_ERR_INVALID_ARG);
+  return -1;
+}
+
+// Gives page `id`, of rank `rank` among the free ones, to the request that wants it.
+template <bool FORK>
+__device__ __forceinline__ void hand_out(const PagesParams& p, const int* prefix, int rank, int id) {
+  const tq_page_pool& pool = p.pool;
+  int lo = 0, hi = p.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= rank) lo = mid; else hi = mid - 1;
+  }
+  const int col = FORK ? p.lens[lo] / pool.page_size : pages_of(p.old_lens[lo], pool.page_size) + rank - prefix[lo];
+  pool.block_table[static_cast<int64_t>(p.rows[lo]) * pool.max_pages + col] = id;
+  pool.refs[id] = 1;
+  if (FORK) p.to[lo] = id;
+}
+
+// Small pools: counts, requests and pages in one block.  A fork leaves prefix[n] = -1 where it changes
+// nothing.
+template <bool FORK>
+__global__ void __launch_bounds__(kSmallThreads) small_assign_kernel(const PagesParams p) {
+  __shared__ int sh[kSmallThreads / 32], prefix[kSmallRequests];
+  __shared__ uint32_t marks[2][kSmallRows / 32];
+  __shared__ uint16_t free_ids[kSmallPages];
+  __shared__ int bad;
+  const int tid = threadIdx.x, words = (p.pool.rows + 31) / 32;
+  for (int i = tid; i < words; i += kSmallThreads) marks[0][i] = marks[1][i] = 0;
+  if (tid == 0) bad = 0;
+  pdl_wait();
+  pdl_trigger();
+  int r[kPer];
+  const int64_t p0 = tid * kPer;
+  load_refs(p.pool, p0, r);
+  __syncthreads();
+  int need = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kSmallThreads) {
+    const int i = i0 + tid;
+    int row = 0, src = 0, want = 0;
+    if (i < p.n) {
+      const bool ok = request<FORK>(p, i, row, src, want);
+      if (!ok) want = 0;
+      if (FORK && ok) mark(marks[1], src);
+      if (!ok || mark(marks[0], row)) bad = 1;
+    }
+    const int before = block_before(want, sh);
+    if (i < p.n) prefix[i] = need + before;
+    need += block_sum<kSmallThreads>(want, sh);
+  }
+  __syncthreads();
+  if (FORK)                                  // a row that is made must not be copied from too
+    for (int i = tid; i < words; i += kSmallThreads)
+      if (marks[0][i] & marks[1][i]) bad = 1;
+  const int mine = count_free(r);
+  int rank = block_before(mine, sh);
+  const int all = block_sum<kSmallThreads>(mine, sh);
+  const bool refused = bad, short_of = refused || all < need;        // (block_sum's barriers stand between)
+  if (tid == 0) {
+    *p.shortfall = refused ? -1 : max(0, need - all);
+    if (refused) report_status(p.status, TQ_ERR_INVALID_ARG);
+    if (FORK) p.prefix[p.n] = short_of ? -1 : need;
+  }
+  if (short_of) return;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (r[k] <= 0) {
+      if (rank < need) free_ids[rank] = static_cast<uint16_t>(p0 + k);
+      ++rank;
+    }
+  if (FORK)
+    for (int i = tid; i < p.n; i += kSmallThreads) {
+      p.from[i] = tail_page(p, i);
+      if (p.lens[i] % p.pool.page_size == 0) p.to[i] = -1;
+    }
+  __syncthreads();
+  for (int k = tid; k < need; k += kSmallThreads) hand_out<FORK>(p, prefix, k, free_ids[k]);
+}
+
 // Blocks 0 .. chunks - 1 hand out the free pages of their chunk; fork has one more block a
 // request, which shares the parent's whole pages.
 template <bool FORK>
@@ -176,26 +287,10 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
       if (threadIdx.x == 0) p.to[i] = -1;
       return;
     }
-    const int full = len / pool.page_size;
-    const int32_t* from = pool.block_table + static_cast<int64_t>(p.src[i]) * pool.max_pages;
-    int32_t* to = pool.block_table + static_cast<int64_t>(p.rows[i]) * pool.max_pages;
-    for (int c = threadIdx.x; c < full; c += kThreads) {
-      const int id = from[c];
-      to[c] = id;
-      if (id >= 0 && id < pool.num_pages) atomicAdd(pool.refs + id, 1);
-      else report_status(p.status, TQ_ERR_INVALID_ARG);
-    }
+    share_pages(p, i);
     if (threadIdx.x == 0) {
-      int id = -1;
-      if (len % pool.page_size) {
-        id = from[full];
-        if (id < 0 || id >= pool.num_pages) {
-          report_status(p.status, TQ_ERR_INVALID_ARG);
-          id = -1;
-        }
-      }
-      p.from[i] = id;
-      if (len % pool.page_size == 0) p.to[i] = -1;
+      p.from[i] = tail_page(p, i);
+      if (len % p.pool.page_size == 0) p.to[i] = -1;
     }
     return;
   }
@@ -205,20 +300,8 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
   load_refs(pool, p0, r);
   int rank = before + block_before(count_free(r), sh);
 #pragma unroll 1
-  for (int k = 0; k < kPer && rank < need; ++k) {
-    if (r[k] > 0) continue;
-    int lo = 0, hi = p.n - 1;                // the request that wants page `rank`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.prefix[mid] <= rank) lo = mid; else hi = mid - 1;
-    }
-    const int id = static_cast<int>(p0 + k);
-    const int col = FORK ? p.lens[lo] / pool.page_size : pages_of(p.old_lens[lo], pool.page_size) + rank - p.prefix[lo];
-    pool.block_table[static_cast<int64_t>(p.rows[lo]) * pool.max_pages + col] = id;
-    pool.refs[id] = 1;
-    if (FORK) p.to[lo] = id;
-    ++rank;
-  }
+  for (int k = 0; k < kPer && rank < need; ++k)
+    if (r[k] <= 0) hand_out<FORK>(p, p.prefix, rank++, static_cast<int>(p0 + k));
 }
 
 __global__ void __launch_bounds__(kThreads) free_kernel(const PagesParams p) {
@@ -288,6 +371,46 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PagesParam
   }
 }
 
+// Compaction of a small pool, both passes in one block.  live: live pages; chunk_free[0]: pages that move.
+__global__ void __launch_bounds__(kSmallThreads) small_compact_kernel(const PagesParams p) {
+  __shared__ int sh[kSmallThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const tq_page_pool& pool = p.pool;
+  int r[kPer];
+  const int64_t p0 = threadIdx.x * kPer;
+  load_refs(pool, p0, r);
+  const int mine = count_free(r);
+  int frank = block_before(mine, sh);
+  const int L = static_cast<int>(pool.num_pages) - block_sum<kSmallThreads>(mine, sh);
+  int low = 0;                               // free pages below L
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) low += r[k] <= 0 && p0 + k < L;
+  const int low_free = block_sum<kSmallThreads>(low, sh);
+  if (threadIdx.x == 0) {
+    *p.live = L;
+    p.chunk_free[0] = low_free;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int id = static_cast<int>(p0) + k;
+    if (id >= pool.num_pages) break;
+    int m = -1;
+    if (r[k] > 0) {
+      m = id;
+      if (id >= L) {
+        const int j = id - frank - (L - low_free);
+        p.from[j] = id;
+        m = -2 - j;
+      }
+    } else {
+      if (id < L) p.to[frank] = id;
+      ++frank;
+    }
+    p.page_map[id] = m;
+  }
+}
+
 template <typename V, int N>
 __device__ __forceinline__ void copy_units(V* dst, const V* src, int units) {
   int i = threadIdx.x;
@@ -301,16 +424,22 @@ __device__ __forceinline__ void copy_units(V* dst, const V* src, int units) {
   for (; i < units; i += kThreads) dst[i] = src[i];
 }
 
-enum : int { COPY_LIST = 0, COPY_FORK = 1, COPY_COMPACT = 2 };
+enum : int { COPY_LIST = 0, COPY_FORK = 1, COPY_COMPACT = 2, COPY_SMALL_FORK = 3, COPY_SMALL_COMPACT = 4 };
 
 // Moves the pages of the pairs in from / to, one slice of one array a step.
-template <int MODE>
+template <int KIND>
 __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
+  constexpr int MODE = KIND == COPY_SMALL_FORK ? COPY_FORK : KIND == COPY_SMALL_COMPACT ? COPY_COMPACT : KIND;
   pdl_wait();
   pdl_trigger();
   const int64_t n_pages = p.pool.num_pages;
   int64_t pairs = p.n;
-  if (MODE == COPY_COMPACT) {
+  if (KIND == COPY_SMALL_FORK) {
+    if (p.prefix[p.n] < 0) return;
+    for (int i = blockIdx.x; i < p.n; i += gridDim.x) share_pages(p, i);
+  }
+  if (KIND == COPY_SMALL_COMPACT) pairs = p.chunk_free[0];
+  if (KIND == COPY_COMPACT) {
     // pages that move: free pages below the live count
     __shared__ int sh[kThreads / 32];
     const int64_t L = *p.live;
@@ -322,6 +451,8 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
       n += p.page_map[q] == -1;
     }
     pairs = block_sum(n, sh);
+  }
+  if (MODE == COPY_COMPACT) {
     // entries of the table, by the map (-2 - j: the page that pair j leads to)
     const int64_t entries = static_cast<int64_t>(p.pool.rows) * p.pool.max_pages;
     for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < entries;
@@ -375,12 +506,23 @@ cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t s) {
   return launch_pdl(free_kernel, dim3(p.n), dim3(kThreads), 0, s, p);
 }
 
+// One block does it (small_assign_kernel).
+static bool is_small(const PagesParams& p) {
+  return p.pool.num_pages <= kSmallPages && p.n <= kSmallRequests && p.pool.rows <= kSmallRows;
+}
+
 cudaError_t launch_pages_reserve(const PagesParams& p, cudaStream_t s) {
+  if (is_small(p)) return launch_pdl(small_assign_kernel<false>, dim3(1), dim3(kSmallThreads), 0, s, p);
   cudaError_t e = launch_pdl(count_kernel<COUNT_RESERVE>, dim3(p.chunks + 1), dim3(kThreads), 0, s, p);
   return e != cudaSuccess ? e : launch_pdl(assign_kernel<false>, dim3(p.chunks), dim3(kThreads), 0, s, p);
 }
 
 cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t s) {
+  if (is_small(p)) {
+    cudaError_t e = launch_pdl(small_assign_kernel<true>, dim3(1), dim3(kSmallThreads), 0, s, p);
+    const unsigned grid = std::max(copy_grid(p.n, p, sms), std::min(static_cast<unsigned>(p.n), 8u * sms));
+    return e != cudaSuccess ? e : launch_pdl(copy_kernel<COPY_SMALL_FORK>, dim3(grid), dim3(kThreads), 0, s, p);
+  }
   cudaError_t e = launch_pdl(count_kernel<COUNT_FORK>, dim3(p.chunks + 1), dim3(kThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(assign_kernel<true>, dim3(p.chunks + p.n), dim3(kThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(copy_kernel<COPY_FORK>, dim3(copy_grid(p.n, p, sms)), dim3(kThreads), 0, s, p);
@@ -388,10 +530,14 @@ cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t s) {
+  const unsigned grid = copy_grid(p.pool.num_pages / 2 + 1, p, sms);
+  if (p.pool.num_pages <= kSmallPages) {
+    cudaError_t e = launch_pdl(small_compact_kernel, dim3(1), dim3(kSmallThreads), 0, s, p);
+    return e != cudaSuccess ? e : launch_pdl(copy_kernel<COPY_SMALL_COMPACT>, dim3(grid), dim3(kThreads), 0, s, p);
+  }
   cudaError_t e = launch_pdl(count_kernel<COUNT_COMPACT>, dim3(p.chunks), dim3(kThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(compact_plan_kernel, dim3(p.chunks), dim3(kThreads), 0, s, p);
-  if (e == cudaSuccess)
-    e = launch_pdl(copy_kernel<COPY_COMPACT>, dim3(copy_grid(p.pool.num_pages / 2 + 1, p, sms)), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(copy_kernel<COPY_COMPACT>, dim3(grid), dim3(kThreads), 0, s, p);
   return e;
 }
 

@@ -177,3 +177,26 @@ def test_packed_records_share_and_move_with_their_pool():
     assert refs.sum().item() == 2 * 5 and torch.equal(run(0), want) and torch.equal(run(1), want)
     K.pages_free(pool, i32([0]), i32([n]))
     assert torch.equal(run(1), want) and refs.max().item() == 1 and K.get_status() == 0
+
+
+@pytest.mark.parametrize("rows,mp,page,pages,widths", [
+    (80, 300, 16, 20011, ((8, torch.int32),)),                          # more pages than one block takes
+    (16400, 2, 32, 9000, ((4, torch.int32),)),                          # more rows
+])
+def test_large_pools_equal_the_oracle(rows, mp, page, pages, widths):
+    r = H.rng(rows + pages)
+    p = Both(r, rows, mp, page, pages, widths)
+    for step in range(4):
+        pick = [int(x) for x in r.permutation(rows)[:min(rows // 2, 1500 if step else 2500)]]
+        p.reserve([i for i in pick if p.lens[i] == 0] or pick[:1], [int(r.integers(0, mp * page + 1)) for i in pick if p.lens[i] == 0]
+                  or [mp * page])
+        p.check()
+        dst = [i for i in range(rows) if p.lens[i] == 0][:40]
+        src = [i for i in range(rows) if p.lens[i]]
+        if dst and src:
+            p.fork([src[int(r.integers(len(src)))] for _ in dst], dst)
+            p.check()
+        p.free([i for i in range(rows) if p.lens[i]][::2])
+        p.compact()
+        p.check()
+    assert K.get_status() == 0
