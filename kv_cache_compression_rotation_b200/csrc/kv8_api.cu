@@ -149,7 +149,7 @@ AttnPlan plan_attn(int dtype, int B, int Hkv, int G, int T, int d, int64_t cap) 
   AttnPlan P{};
   const int64_t R = static_cast<int64_t>(T) * G;
   P.prefill = dtype != TQ_F32 && R > kKv8DecodeRows;
-  const int rows = P.prefill ? kKv8PrefillRows : kKv8DecodeRows, tile = P.prefill ? 128 : 32;
+  const int rows = P.prefill ? kKv8PrefillRows : kKv8DecodeRows, tile = P.prefill ? 128 : kv8_decode_tile(d);
   P.RG = static_cast<int>((R + rows - 1) / rows);
   P.VB = static_cast<int64_t>(B) * P.RG;
   // the tiles of a launch are counted in 32 bits

@@ -74,7 +74,7 @@ struct Eight {
 };
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8AppendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_append_kernel(const Kv8AppendParams p) {
   constexpr int LPR = D / 8;          // lanes a row
   constexpr int RPP = 32 / LPR;       // rows a pass
   constexpr int NP = kKv8Block / RPP;

@@ -4,7 +4,7 @@
 //   l_t = scale q.k^_t (capped, biased),  out = sum_t softmax(l)_t v^_t,  lse = ln sum_t e^{l_t}
 //
 // Bytes bound it: each token of a key head is 2 d codes and 2 / 16 scales, read once for all its
-// query rows.  The launch has one CTA an SM; the tiles of 32 tokens of all (sequence, key head)
+// query rows.  The launch has one CTA an SM; the tiles of 32 (d = 64: 64) tokens of all (sequence, key head)
 // pairs form one line that is cut into equal runs, one a CTA, so ragged lengths and few long
 // sequences load every SM alike.  A pair that one run covers is finished in the CTA; the others
 // leave at most two partial results a CTA, joined by a second, small kernel.
@@ -33,7 +33,8 @@ namespace {
 
 // Warps of a CTA.  Their instructions' latency bounds a tile, so as many as the registers allow.
 __host__ __device__ constexpr int warps_of(int NT, int W) { return NT == 1 && W == 1 ? 12 : 8; }
-constexpr int kTile = 32;                  // tokens
+// Tokens of a tile: what it costs a warp beside its tokens is shared by 8 KB of codes.
+__host__ __device__ constexpr int tile_of(int D) { return kv8_decode_tile(D); }
 constexpr int kMinTiles = 8;               // a CTA's tiles, where there is little work
 // Outputs of 8 * NT rows on their way to the sum over the warps: a lane of the product holds two
 // neighbouring dims of row 2 (lane % 4) + c and eighth lane / 4 of the dims; the padding keeps the
@@ -41,18 +42,18 @@ constexpr int kMinTiles = 8;               // a CTA's tiles, where there is litt
 __host__ __device__ constexpr int eighth(int D) { return D / 8 + 2; }
 __host__ __device__ constexpr int out_stride(int D) { return 8 * eighth(D) + 4; }
 
-__host__ __device__ constexpr int ring_stages(int D, int NT, int W) { return D == 64 ? 4 : (NT == 1 && W == 2 ? 3 : 2); }
-__host__ __device__ constexpr uint32_t stage_bytes(int D) { return 2u * kTile * D; }
+__host__ __device__ constexpr int ring_stages(int NT, int W) { return warps_of(NT, W) == 8 ? 3 : 2; }
+__host__ __device__ constexpr uint32_t stage_bytes(int D) { return 2u * tile_of(D) * D; }
 
 struct DecodeSmem {
   uint32_t scales, bars, lo, hi, pref, ml, fin, o, total;
 };
 __host__ __device__ constexpr DecodeSmem decode_smem(int D, int NT, int W) {
-  const int ns = ring_stages(D, NT, W), kWarps = warps_of(NT, W);
+  const int ns = NT == 2 ? 2 : ring_stages(NT, W), kWarps = warps_of(NT, W);
   DecodeSmem L{};
   uint32_t at = kWarps * ns * stage_bytes(D);
   L.o = at; at += 4u * 8 * NT * out_stride(D) * 4;             // four warps' outputs
-  L.scales = at; at += kWarps * ns * 16;
+  L.scales = at; at += kWarps * ns * (tile_of(D) / kKv8Block) * 8;
   L.bars = at; at += kWarps * ns * 8;
   L.ml = at; at += kWarps * (16 * 2 + 1) * 4;                  // m, l of 16 rows and E
   L.fin = at; at += 16 * 2 * 4;                                // 1 / sum and lse of 16 rows
@@ -119,8 +120,9 @@ template <int D, int NT, int W>
 __global__ void __launch_bounds__(warps_of(NT, W) * 32, 1)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const Kv8AttnParams p) {
-  constexpr int NS = ring_stages(D, NT, W), kWarps = warps_of(NT, W);
+  constexpr int NS = NT == 2 ? 2 : ring_stages(NT, W), kWarps = warps_of(NT, W);
   constexpr uint32_t SB = stage_bytes(D);
+  constexpr int kTile = tile_of(D), NB = kTile / kKv8Block;            // tokens and blocks of a tile
   constexpr DecodeSmem L = decode_smem(D, NT, W);
   constexpr int KJ = D / 64;               // 64-dim halves of a row
   constexpr int MT = D / 16;               // 16-dim rows of the output product
@@ -140,10 +142,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   const int g = lane >> 2, qd = lane & 3;
   const uint32_t ring = base + warp * NS * SB;
   const uint32_t bar0 = base + L.bars + warp * NS * 8;
-  const uint32_t sc0 = base + L.scales + warp * NS * 16;
+  const uint32_t sc0 = base + L.scales + warp * NS * NB * 8;
   const int ppb = static_cast<int>(p.map.page / kKv8Block);
   if (lane == 0)
-    for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 5);
+    for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1 + 2 * NB);
   if (tid == 0) {
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -178,54 +180,88 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   // ---- issue side: the warp's share of the tiles of the CTA's runs
   int64_t iu = u0;
   Kv8Run ir{};
-  int ij = warp, issued = 0, used = 0, id = 0, place = 0;
-  // Moves to the run of the warp's next tile and asks for the page of its block lane % 2.
+  int ij = warp, issued = 0, used = 0;
+  // Lane k (of NB) follows block k of the warp's tiles: its page's column and its place in the page.
+  int blk = 0, col = 0, in = 0, b_lo = 0, b_hi = 0, seq = 0;
+  const int32_t* row = nullptr;
+  const int step_col = kWarps * NB / ppb, step_in = kWarps * NB - step_col * ppb;
+  struct Next {                              // the warp's next tile: page and place of the lane's block, key head
+    int id, place, h;                        // h < 0: no more
+  };
   auto ask = [&]() {
+    Next n{0, 0, -1};
+    bool moved = false;
     while (ij >= ir.tiles) {
       ij -= ir.tiles;
       iu += ir.units;
-      if (iu >= u1) return;
+      if (iu >= u1) return n;
       ir = kv8_run_at(iu, u1, s_pref, VB, Hkv, p.run_cost);
+      moved = true;
     }
-    if (lane < 4) {
-      // a block outside the visible tokens may have no page: the nearest visible one instead
-      const int lo = s_lo[ir.v], hi = s_hi[ir.v], b = (p.v0 + ir.v) / p.RG;
-      const int blk = min(max((lo / kTile + ir.tile + ij) * 2 + (lane & 1), lo / kKv8Block), (hi - 1) / kKv8Block);
-      const int col = blk / ppb;
-      place = blk - col * ppb;
-      id = p.map.table ? __ldg(p.map.table + static_cast<int64_t>(b) * p.map.max_pages + col) : b;
+    if (moved) {
+      const int lo = s_lo[ir.v];
+      seq = (p.v0 + ir.v) / p.RG;
+      b_lo = lo / kKv8Block;
+      b_hi = (s_hi[ir.v] - 1) / kKv8Block;
+      row = p.map.table ? p.map.table + static_cast<int64_t>(seq) * p.map.max_pages : nullptr;
+      blk = (lo / kTile + ir.tile + ij) * NB + lane % NB;
+      col = blk / ppb;
+      in = blk - col * ppb;
+    } else {
+      blk += kWarps * NB;
+      col += step_col;
+      in += step_in;
+      if (in >= ppb) {
+        in -= ppb;
+        ++col;
+      }
     }
+    int c = col;
+    n.place = in;
+    if (blk < b_lo || blk > b_hi) {          // it may have no page: the nearest visible block instead
+      const int x = blk < b_lo ? b_lo : b_hi;
+      c = x / ppb;
+      n.place = x - c * ppb;
+    }
+    n.id = row ? __ldg(row + c) : seq;
+    n.h = ir.h;
+    ij += kWarps;
+    return n;
   };
-  auto issue = [&]() {
-    if (iu >= u1) return;
+  auto issue = [&](Next n) {
+    if (n.h < 0) return;
     const int st = issued % NS;
     const uint32_t bar = bar0 + 8 * st, dst = ring + st * SB;
-    if (lane < 4) {
-      if (id < 0 || id >= p.map.num_pages) {
-        report_status(p.status, TQ_ERR_INVALID_ARG);
-        id = 0;
+    if (n.id < 0 || n.id >= p.map.num_pages) {
+      report_status(p.status, TQ_ERR_INVALID_ARG);
+      n.id = 0;
+    }
+    // (a side has fewer than 2^31 records)
+    const int rec = (n.id * Hkv + n.h) * static_cast<int>(p.map.page) + n.place * kKv8Block;
+    if (lane == 0) mbar_expect_tx(bar, SB);
+    __syncwarp();
+    if (lane < 2 * NB) {
+      if (lane < NB) {
+        tma_load_2d(dst + lane * kKv8Block * D, &kmap, 0, rec, bar);
+        tma_load_2d(dst + (kTile + lane * kKv8Block) * D, &vmap, 0, rec, bar);
       }
-      const int64_t rec = (static_cast<int64_t>(id) * Hkv + ir.h) * p.map.page + place * kKv8Block;
-      if (lane == 0) mbar_expect_tx(bar, SB);
-      __syncwarp(0xfu);
-      if (lane < 2) {
-        const uint32_t off = (lane & 1) * kKv8Block * D;
-        const int row = static_cast<int>(rec);
-        tma_load_2d(dst + off, &kmap, 0, row, bar);
-        tma_load_2d(dst + kTile * D + off, &vmap, 0, row, bar);
-      }
-      const float* src = ((lane & 2) ? p.vscales : p.kscales) + rec / kKv8Block;
-      const uint32_t to = sc0 + st * 16 + lane * 4;
+      const float* src = (lane < NB ? p.kscales : p.vscales) + rec / kKv8Block;
+      const uint32_t to = sc0 + (st * 2 * NB + lane) * 4;
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
     }
     __syncwarp();
     ++issued;
-    ij += kWarps;
-    ask();
   };
-  ask();
-  for (int s = 0; s < NS; ++s) issue();
+  Next next;
+  {
+    Next n[NS];                              // (all asked for before the first is needed)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) n[s] = ask();
+    next = ask();
+#pragma unroll
+    for (int s = 0; s < NS; ++s) issue(n[s]);
+  }
 
   // ---- consume side, one (sequence, key head) at a time
   int cj = warp;
@@ -334,14 +370,17 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       ++used;
       const int t0 = (s_lo[sp.v] / kTile + sp.tile + cj) * kTile;
       const bool masked = t0 < in_lo || t0 + kTile > in_hi;
-      float4 sc;                                 // key scales, value scales of the two blocks
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(sc.x), "=f"(sc.y), "=f"(sc.z), "=f"(sc.w)
-                   : "r"(sc0 + st * 16));
+      float ksc[NB], vsc[NB];                    // scales of the blocks
+#pragma unroll
+      for (int i = 0; i < NB; i += 2) {
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(ksc[i]), "=f"(ksc[i + 1]) : "r"(sc0 + (st * 2 * NB + i) * 4));
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vsc[i]), "=f"(vsc[i + 1]) : "r"(sc0 + (st * 2 * NB + NB + i) * 4));
+      }
 
       // scores
-      float s[2][NT][4];
+      float s[NB][NT][4];
 #pragma unroll
-      for (int bl = 0; bl < 2; ++bl) {
+      for (int bl = 0; bl < NB; ++bl) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -369,8 +408,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
-      for (int bl = 0; bl < 2; ++bl) {
-        const float kscale = bl ? sc.y : sc.x;
+      for (int bl = 0; bl < NB; ++bl) {
+        const float kscale = ksc[bl];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -385,9 +424,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           }
       }
       // the running maxima, and the largest value scale
-      const int e0 = static_cast<int>((__float_as_uint(sc.z) >> 23) & 0xffu);
-      const int e1 = static_cast<int>((__float_as_uint(sc.w) >> 23) & 0xffu);
-      const int E1 = max(E, max(e0, e1));
+      int E1 = E;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) E1 = max(E1, static_cast<int>((__float_as_uint(vsc[i]) >> 23) & 0xffu));
       bool grown = E1 > E;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -416,10 +455,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         E = E1;
       }
       // probabilities, times their block's value scale, as the second product's columns
-      uint32_t pf[W][2][NT][2];
+      uint32_t pf[W][NB][NT][2];
 #pragma unroll
-      for (int bl = 0; bl < 2; ++bl) {
-        const int ev = (bl ? e1 : e0) - E;
+      for (int bl = 0; bl < NB; ++bl) {
+        const int ev = static_cast<int>((__float_as_uint(vsc[bl]) >> 23) & 0xffu) - E;
         const float f = ev < -120 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 15 + ev) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -441,7 +480,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       }
       // O^T += V^T P^T: lane g holds dims (D / 8) g .. of the four tokens 2 qd, + 1, + 8, + 9
 #pragma unroll
-      for (int bl = 0; bl < 2; ++bl) {
+      for (int bl = 0; bl < NB; ++bl) {
         constexpr int VW = D / 32;             // words a lane and token
         uint32_t v4[4][VW];
 #pragma unroll
@@ -476,7 +515,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
       }
       __syncwarp();
-      issue();                                  // into the stage just read
+      issue(next);                              // into the stage just read
+      next = ask();
     }
 
     cj -= sp.tiles;

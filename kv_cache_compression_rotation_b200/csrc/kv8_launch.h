@@ -61,6 +61,7 @@ struct Kv8AttnParams {
 // Groups of 16 rows a key head (decode; fp32 queries).  kmap / vmap: the codes as [records][d]
 // bytes in boxes of 16 rows.
 constexpr int kKv8DecodeRows = 16;
+__host__ __device__ constexpr int kv8_decode_tile(int d) { return d == 64 ? 64 : 32; }       // tokens
 constexpr int kKv8DecodeMaxVB = 1024;                 // virtual sequences a launch
 cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
                               cudaStream_t s);
