@@ -448,16 +448,14 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
           }
           return formed ? fmaxf(a, b) : fmaxf(a * (sc[2 * c] * rowc), b * (sc[2 * c + 1] * rowc));
         };
+        tmem_ld32(ts + 64, s2);
+        tmem_ld32(ts + 96, s3);
         tmem_wait_ld();
         pin(s0);
         pin(s1);
-        tmem_ld32(ts + 64, s2);
-        tmem_ld32(ts + 96, s3);
-        float mx = fmaxf(top(s0, 0), top(s1, 1));
-        tmem_wait_ld();
         pin(s2);
         pin(s3);
-        mx = fmaxf(mx, fmaxf(top(s2, 2), top(s3, 3)));
+        const float mx = fmaxf(fmaxf(top(s0, 0), top(s1, 1)), fmaxf(top(s2, 2), top(s3, 3)));
         // ---- the reference, and what was summed against the old one and the old E
         const bool grow = mx > m + kLazy || m == -INFINITY;
         const float m1 = grow ? fmaxf(m, mx) : m;
