@@ -493,7 +493,7 @@ typedef struct {
  */
 typedef struct {
   float scale;
-  float softcap;          /* 0 = none */
+  float softcap;          /* 0 = none, else 1e-30..1e30 */
   const float* slopes;
   int32_t window;         /* 0 = none */
   const int32_t* first;

@@ -43,7 +43,7 @@ constexpr int kSlot = 3 * kBlocks + 4;       // key scales, exponents f of the p
 // 775 us with 2, 589 with 4, 605 with 7; where the tiles cost more, capped d = 64: 114 with 2, 125 with 4.)
 __host__ __device__ constexpr int run_cost(bool gen) { return gen ? 2 : 4; }
 // Registers a thread of the roles' warpgroups; the launch has 128 for each of 512 threads.
-constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsRest = 48, kRegsLaunch = 128;
+constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsRest = 56, kRegsLaunch = 128;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsRest <= 4 * kRegsLaunch, "registers");
 constexpr int kScouts = 32;                  // the warp that prepares runs
 

@@ -191,3 +191,14 @@ def test_binding_refuses_what_the_library_cannot_see():
         K.kv8_decode_attn(x[..., :64].contiguous()[:, :, 0], lens, k, k, 1, Nmax=32)
     with pytest.raises(ValueError):
         K.kv8_decode_attn(x[:, :, 0], lens, k, k, 1, Nmax=32, scoring=K.Scoring(slopes=torch.zeros(3)))
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("kw,code", [
+    (dict(sc=scoring(softcap=1e-31)), INVALID), (dict(sc=scoring(softcap=2e30)), INVALID), (dict(sc=scoring(softcap=-1.0)), INVALID),
+    # 2^30 tokens a sequence by way of pages named often, times 64 key heads
+    (dict(Hq=64, Hkv=64, pages=pages(page=1 << 20, mp=1 << 10, num=16)), UNSUPPORTED),
+])
+def test_attention_refuses_caps_and_counts_out_of_range(lib, prefill, kw, code):
+    assert attn(lib, prefill, wsb=1 << 40, **kw) == code
+    assert lib.tq_last_error()
