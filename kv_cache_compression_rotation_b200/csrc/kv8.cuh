@@ -131,10 +131,10 @@ __device__ __forceinline__ void kv8_prefix(int* pref, int VB) {
   if (lane == 0) pref[0] = 0;
 }
 
-// A CTA that starts inside a key head's units says so for the kernel that joins: plan[c] = {v, h, c0,
-// c1}, the CTAs that worked on it, if c is the second of them, else v = -1.  A key head has `cost`
-// units before its tiles.
-__device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1, int64_t per, const int* pref, int VB, int Hkv,
+// A part (a CTA's or a warp's) that starts inside a key head's units says so for the kernel that joins:
+// plan[c] = {v, h, c0, c1}, the parts that the key head is cut into, if c is the second of them, else
+// v = -1.  A key head has `cost` units before its tiles.
+__device__ __forceinline__ void kv8_plan_split(int* plan, int c, int64_t u0, int64_t u1, int64_t per, const int* pref, int VB, int Hkv,
                                                int cost) {
   int4 s = make_int4(-1, 0, 0, 0);
   if (u0 < u1 && u0 > 0) {
@@ -142,15 +142,15 @@ __device__ __forceinline__ void kv8_plan_split(int* plan, int64_t u0, int64_t u1
     const int64_t start = u0 - p.tile;
     s.z = static_cast<int>((start + cost) / per);
     s.w = static_cast<int>((start + p.n - 1) / per);
-    if (p.tile > 0 && s.z + 1 == static_cast<int>(blockIdx.x)) {
+    if (p.tile > 0 && s.z + 1 == c) {
       s.x = p.v;
       s.y = p.h;
     }
   }
-  reinterpret_cast<int4*>(plan)[blockIdx.x] = s;
+  reinterpret_cast<int4*>(plan)[c] = s;
 }
 
-// Tiles [tile, tile + tiles) of the n of key head h of virtual sequence v: what a CTA does from unit u
+// Tiles [tile, tile + tiles) of the n of key head h of virtual sequence v: what a part does from unit u
 // of the line to u1 or to the end of the key head, which has `cost` units before those of its tiles.
 struct Kv8Run {
   int v, h, tile, tiles, n, units;

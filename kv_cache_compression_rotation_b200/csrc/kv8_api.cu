@@ -136,6 +136,7 @@ tq_status prepare_append(const Append& a, int dtype, int B, int Hkv, int d, cons
 // ---- attention
 struct AttnPlan {
   bool prefill;        // the tensor-memory kernel
+  bool team;           // else a CTA's warps share its runs, or each has its own
   int64_t VB;          // virtual sequences: row groups of a sequence
   int RG, grid, max_vb, run_cost;
   size_t off_lse, off_plan, bytes;
@@ -158,15 +159,23 @@ AttnPlan plan_attn(int dtype, int B, int Hkv, int G, int T, int d, int64_t cap) 
   P.max_vb = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(P.prefill ? kKv8PrefillMaxVB : kKv8DecodeMaxVB,
                                                                      (1ll << 30) / (cap / tile + 2))));
   const int sms = sm_count();
-  // decode: eight tiles a CTA at least, one a warp
-  const int64_t tiles = std::min<int64_t>(P.VB, P.max_vb) * Hkv * (cap / tile + 2), least = P.prefill ? 1 : 8;
+  const int64_t pairs = std::min<int64_t>(P.VB, P.max_vb) * Hkv, tiles = pairs * (cap / tile + 2);
+  const int warps = kv8_decode_warps(R, dtype == TQ_F32);
+  // Decode: where the (sequence, key head) pairs are as many as the SMs, each warp takes its own, which
+  // needs no joining in the CTA (2048 pairs of up to 512 tokens: 46 us against 130; 192 of up to 8192,
+  // d = 64: 40 against 45); else a CTA's warps share one, so that fewer partial results are left to join
+  // (64 pairs of 4096 tokens: 26 us against 31).
+  P.team = !P.prefill && pairs < sms;
+  const int64_t least = P.team ? 8 : 1;
   P.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, (tiles + least - 1) / least)));
-  // A key head's run costs a decode CTA about 16 tiles beside its own (q, and the joining of the warps),
-  // but where a CTA gets few tiles the cut would be the cost's, not the tiles'.
-  P.run_cost = static_cast<int>(std::clamp<int64_t>((tiles / P.grid - 16) / 4, 0, 16));
-  P.off_lse = static_cast<size_t>(2) * P.grid * rows * d * 4;
-  P.off_plan = P.off_lse + up16(static_cast<size_t>(2) * P.grid * rows * 4);
-  P.bytes = P.off_plan + up16((std::max(kKv8DecodeMaxVB, kKv8PrefillMaxVB) + 3) * 4);
+  const int64_t parts = P.prefill || P.team ? P.grid : static_cast<int64_t>(P.grid) * warps;
+  // What a key head's run costs beside its tiles, in tiles: for a CTA q and the joining of the warps, for
+  // a warp q.  Where a part gets few tiles the cut would be the cost's, not the tiles'.
+  P.run_cost = static_cast<int>(P.team ? std::clamp<int64_t>((tiles / parts - 16) / 2, 0, 32)
+                                       : std::clamp<int64_t>((tiles / parts - 2) / 2, 0, 2));
+  P.off_lse = static_cast<size_t>(2) * parts * rows * d * 4;
+  P.off_plan = P.off_lse + up16(static_cast<size_t>(2) * parts * rows * 4);
+  P.bytes = P.off_plan + static_cast<size_t>(parts) * 16;
   return P;
 }
 
@@ -296,7 +305,7 @@ tq_status run_attn(const AttnCall& c) {
     p.v0 = static_cast<int>(v);
     p.VB = static_cast<int>(std::min<int64_t>(P.max_vb, P.VB - v));
     e = P.prefill ? launch_kv8_prefill(c.kc.codes, c.vc.codes, p, c.d, P.grid, c.stream)
-                  : launch_kv8_decode(kmap, vmap, p, c.d, P.grid, c.stream);
+                  : launch_kv8_decode(kmap, vmap, p, c.d, P.team, P.grid, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
   return TQ_OK;

@@ -31,10 +31,9 @@
 namespace tq {
 namespace {
 
-// Warps of a CTA.  Their instructions' latency bounds a tile, so as many as the registers allow.
-__host__ __device__ constexpr int warps_of(int NT, int W) { return NT == 1 && W == 1 ? 12 : 8; }
 // Tokens of a tile: what it costs a warp beside its tokens is shared by 8 KB of codes.
 __host__ __device__ constexpr int tile_of(int D) { return kv8_decode_tile(D); }
+__host__ __device__ constexpr int warps_of(int NT, int W) { return kv8_decode_warps(8 * NT, W == 2); }
 constexpr int kMinTiles = 8;               // a CTA's tiles, where there is little work
 // Outputs of 8 * NT rows on their way to the sum over the warps: a lane of the product holds two
 // neighbouring dims of row 2 (lane % 4) + c and eighth lane / 4 of the dims; the padding keeps the
@@ -116,11 +115,13 @@ __device__ __forceinline__ void store4(void* out, int dtype, int64_t at, float2 
   }
 }
 
-template <int D, int NT, int W>
+// TEAM: a CTA's warps share each run, else each warp has runs of its own.
+template <int D, int NT, int W, bool TEAM>
 __global__ void __launch_bounds__(warps_of(NT, W) * 32, 1)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const Kv8AttnParams p) {
   constexpr int NS = NT == 2 ? 2 : ring_stages(NT, W), kWarps = warps_of(NT, W);
+  constexpr int STEP = TEAM ? kWarps : 1;  // a warp takes every STEP-th tile of its runs
   constexpr uint32_t SB = stage_bytes(D);
   constexpr int kTile = tile_of(D), NB = kTile / kKv8Block;            // tokens and blocks of a tile
   constexpr DecodeSmem L = decode_smem(D, NT, W);
@@ -172,19 +173,21 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   if (warp == 0) kv8_prefix(s_pref, VB);
   __syncthreads();
   const int64_t total = static_cast<int64_t>(s_pref[VB]) * Hkv;
-  const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinTiles));
-  const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
+  // Neighbouring parts of the line go to different SMs, so that a short one is spread over all.
+  const int parts = TEAM ? gridDim.x : gridDim.x * kWarps, part = TEAM ? blockIdx.x : warp * gridDim.x + blockIdx.x;
+  const int64_t per = max((total + parts - 1) / parts, static_cast<int64_t>(TEAM ? kMinTiles : 1));
+  const int64_t u0 = min(total, per * part), u1 = min(total, u0 + per);
   if (p.appended) pdl_wait();
   pdl_trigger();
 
   // ---- issue side: the warp's share of the tiles of the CTA's runs
   int64_t iu = u0;
   Kv8Run ir{};
-  int ij = warp, issued = 0, used = 0;
+  int ij = TEAM ? warp : 0, issued = 0, used = 0;
   // Lane k (of NB) follows block k of the warp's tiles: its page's column and its place in the page.
   int blk = 0, col = 0, in = 0, b_lo = 0, b_hi = 0, seq = 0;
   const int32_t* row = nullptr;
-  const int step_col = kWarps * NB / ppb, step_in = kWarps * NB - step_col * ppb;
+  const int step_col = STEP * NB / ppb, step_in = STEP * NB - step_col * ppb;
   struct Next {                              // the warp's next tile: page and place of the lane's block, key head
     int id, place, h;                        // h < 0: no more
   };
@@ -208,7 +211,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       col = blk / ppb;
       in = blk - col * ppb;
     } else {
-      blk += kWarps * NB;
+      blk += STEP * NB;
       col += step_col;
       in += step_in;
       if (in >= ppb) {
@@ -225,7 +228,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     n.id = row ? __ldg(row + c) : seq;
     n.h = ir.h;
-    ij += kWarps;
+    ij += STEP;
     return n;
   };
   auto issue = [&](Next n) {
@@ -264,7 +267,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   }
 
   // ---- consume side, one (sequence, key head) at a time
-  int cj = warp;
+  int cj = TEAM ? warp : 0;
   bool dead = false;
   for (int64_t u = u0; u < u1;) {
     const Kv8Run sp = kv8_run_at(u, u1, s_pref, VB, Hkv, p.run_cost);
@@ -361,7 +364,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.f;
     int E = 1;                                   // largest value-scale exponent so far (biased)
 
-    for (; cj < sp.tiles; cj += kWarps) {
+    for (; cj < sp.tiles; cj += STEP) {
       const int st = used % NS;
       const uint32_t bar = bar0 + 8 * st, ks_a = ring + st * SB, vs_a = ks_a + kTile * D;
       if (!dead && !mbar_wait(bar, (used / NS) & 1, p.wait_limit, p.status, abort_flag)) dead = true;
@@ -520,99 +523,133 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
 
     cj -= sp.tiles;
-    // ---- join the warps: common maximum and value scale, then sums in a fixed order
+    const bool whole = sp.tiles == sp.n;
+    const int slot = part * 2 + (sp.tile == 0 ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
-        if (g == 0) {
-          s_ml[warp * 33 + nt * 8 + 2 * qd + c] = m[nt][c];
-          s_ml[warp * 33 + 16 + nt * 8 + 2 * qd + c] = l[nt][c];
+    if constexpr (!TEAM) {
+      // ---- the warp's result: a lane has D / 8 neighbouring dims of each of its rows
+      const float unit = __uint_as_float(static_cast<uint32_t>(E) << 23);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rl = nt * 8 + 2 * qd + c, r = r0 + rl, col = (D / 8) * g;
+          if (r >= R) continue;
+          const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * 32768.f);
+          const float ls2 = l[nt][c] == 0.f ? -INFINITY : m[nt][c] + __log2f(l[nt][c]);
+          const int i = r / p.G;
+          const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
+          if (g == 0) {
+            if (!whole) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
+            else if (p.lse) p.lse[row] = ls2 * kLn2;
+          }
+          // (in units of 2^(E - 127 - 15); two factors, so that neither leaves the normal range)
+#pragma unroll
+          for (int k = 0; k < MT; k += 2) {
+            const float2 x = make_float2(acc[k][nt][c] * inv * unit, acc[k][nt][2 + c] * inv * unit);
+            const float2 y = make_float2(acc[k + 1][nt][c] * inv * unit, acc[k + 1][nt][2 + c] * inv * unit);
+            if (whole) store4<W>(p.out, p.dtype, row * D + col + 2 * k, x, y);
+            else
+              *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + col + 2 * k) =
+                  make_float4(x.x, x.y, y.x, y.y);
+          }
         }
-      }
-    if (lane == 0) s_ml[warp * 33 + 32] = static_cast<float>(E);
-    __syncthreads();
-    float Em = 1.f;
+    } else {
+      // ---- join the warps: common maximum and value scale, then sums in a fixed order
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) Em = fmaxf(Em, s_ml[w * 33 + 32]);
-    const float unit = __uint_as_float(static_cast<uint32_t>(Em) << 23);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * qd + c;
-        float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w * 33 + r]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) ll += s_ml[w * 33 + 16 + r] * ex2(s_ml[w * 33 + r] - ref);
-        if (warp == 0 && g == 0) {
-          s_fin[2 * r] = ll == 0.f ? 0.f : 1.f / (ll * 32768.f);
-          s_fin[2 * r + 1] = ll == 0.f ? -INFINITY : mm + __log2f(ll);
+        for (int c = 0; c < 2; ++c) {
+          if (g == 0) {
+            s_ml[warp * 33 + nt * 8 + 2 * qd + c] = m[nt][c];
+            s_ml[warp * 33 + 16 + nt * 8 + 2 * qd + c] = l[nt][c];
+          }
         }
-        const float a = ex2(m[nt][c] - ref + (static_cast<float>(E) - Em));
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          acc[i][nt][c] *= a;
-          acc[i][nt][2 + c] *= a;
-        }
-      }
-    // The last four warps leave their outputs, four by four the others add theirs to them; then every
-    // thread sums four.
-    constexpr int RS = out_stride(D);
-#pragma unroll
-    for (int four = kWarps / 4 - 1; four >= 0; --four) {
-      if (warp / 4 == four) {
-        float* o = s_o + (warp & 3) * 8 * NT * RS + eighth(D) * g;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float2* at = reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * RS + 2 * i);
-              float2 x = make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
-              if (four < kWarps / 4 - 1) {
-                x.x += at->x;
-                x.y += at->y;
-              }
-              *at = x;
-            }
-      }
+      if (lane == 0) s_ml[warp * 33 + 32] = static_cast<float>(E);
       __syncthreads();
-    }
-    const bool whole = sp.tiles == sp.n;
-    const int slot = blockIdx.x * 2 + (sp.tile == 0 ? 1 : 0);
-    for (int e = tid; e < 8 * NT * (D / 4); e += kWarps * 32) {
-      const int rl = e / (D / 4), col = (e - rl * (D / 4)) * 4, r = r0 + rl;
-      if (r >= R) break;
-      const float* o = s_o + rl * RS + eighth(D) * (col / (D / 8)) + col % (D / 8);
-      float2 x = make_float2(0.f, 0.f), y = x;
+      float Em = 1.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 a = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS);
-        const float2 c = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS + 2);
-        x.x += a.x; x.y += a.y; y.x += c.x; y.y += c.y;
+      for (int w = 0; w < kWarps; ++w) Em = fmaxf(Em, s_ml[w * 33 + 32]);
+      const float unit = __uint_as_float(static_cast<uint32_t>(Em) << 23);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = nt * 8 + 2 * qd + c;
+          float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w * 33 + r]);
+          const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) ll += s_ml[w * 33 + 16 + r] * ex2(s_ml[w * 33 + r] - ref);
+          if (warp == 0 && g == 0) {
+            s_fin[2 * r] = ll == 0.f ? 0.f : 1.f / (ll * 32768.f);
+            s_fin[2 * r + 1] = ll == 0.f ? -INFINITY : mm + __log2f(ll);
+          }
+          const float a = ex2(m[nt][c] - ref + (static_cast<float>(E) - Em));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            acc[i][nt][c] *= a;
+            acc[i][nt][2 + c] *= a;
+          }
+        }
+      // The last four warps leave their outputs, four by four the others add theirs to them; then every
+      // thread sums four.
+      constexpr int RS = out_stride(D);
+#pragma unroll
+      for (int four = kWarps / 4 - 1; four >= 0; --four) {
+        if (warp / 4 == four) {
+          float* o = s_o + (warp & 3) * 8 * NT * RS + eighth(D) * g;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float2* at = reinterpret_cast<float2*>(o + (nt * 8 + 2 * qd + c) * RS + 2 * i);
+                float2 x = make_float2(acc[i][nt][c], acc[i][nt][2 + c]);
+                if (four < kWarps / 4 - 1) {
+                  x.x += at->x;
+                  x.y += at->y;
+                }
+                *at = x;
+              }
+        }
+        __syncthreads();
       }
-      // the sums are in units of 2^(Em - 127 - 15); two factors, so that neither leaves the normal range
-      const float inv = s_fin[2 * rl], ls2 = s_fin[2 * rl + 1];
-      x.x = x.x * inv * unit; x.y = x.y * inv * unit; y.x = y.x * inv * unit; y.y = y.y * inv * unit;
-      if (whole) {
-        const int i = r / p.G;
-        const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
-        if (p.lse && col == 0) p.lse[row] = ls2 * kLn2;
-        store4<W>(p.out, p.dtype, row * D + col, x, y);
-      } else {
-        if (col == 0) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
-        *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + col) =
-            make_float4(x.x, x.y, y.x, y.y);
+      for (int e = tid; e < 8 * NT * (D / 4); e += kWarps * 32) {
+        const int rl = e / (D / 4), col = (e - rl * (D / 4)) * 4, r = r0 + rl;
+        if (r >= R) break;
+        const float* o = s_o + rl * RS + eighth(D) * (col / (D / 8)) + col % (D / 8);
+        float2 x = make_float2(0.f, 0.f), y = x;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 a = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS);
+          const float2 c = *reinterpret_cast<const float2*>(o + w * 8 * NT * RS + 2);
+          x.x += a.x; x.y += a.y; y.x += c.x; y.y += c.y;
+        }
+        // the sums are in units of 2^(Em - 127 - 15); two factors, so that neither leaves the normal range
+        const float inv = s_fin[2 * rl], ls2 = s_fin[2 * rl + 1];
+        x.x = x.x * inv * unit; x.y = x.y * inv * unit; y.x = y.x * inv * unit; y.y = y.y * inv * unit;
+        if (whole) {
+          const int i = r / p.G;
+          const int64_t row = (static_cast<int64_t>(b) * p.Hq + sp.h * p.G + (r - i * p.G)) * p.T + i;
+          if (p.lse && col == 0) p.lse[row] = ls2 * kLn2;
+          store4<W>(p.out, p.dtype, row * D + col, x, y);
+        } else {
+          if (col == 0) p.part_lse[slot * kKv8DecodeRows + rl] = ls2;
+          *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kKv8DecodeRows + rl) * D + col) =
+              make_float4(x.x, x.y, y.x, y.y);
+        }
       }
     }
   }
-  if (blockIdx.x > 0 && tid == 0) kv8_plan_split(p.plan, u0, u1, per, s_pref, VB, Hkv, p.run_cost);
+  if (part > 0 && (TEAM ? tid : lane) == 0) kv8_plan_split(p.plan, part, u0, u1, per, s_pref, VB, Hkv, p.run_cost);
   // ---- groups that see nothing
   for (int v = blockIdx.x; v < VB; v += gridDim.x) {
     if (s_pref[v + 1] != s_pref[v]) continue;
@@ -675,30 +712,36 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Kv8AttnParam
   }
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, bool TEAM>
 cudaError_t go(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
-  auto k = kv8_decode_kernel<D, NT, W>;
+  auto k = kv8_decode_kernel<D, NT, W, TEAM>;
   constexpr uint32_t smem = decode_smem(D, NT, W).total;
   static std::atomic<uint64_t> seen{0};
   cudaError_t e = allow_smem(k, smem, seen);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(grid), dim3(warps_of(NT, W) * 32), smem, s, km, vm, p);
-  if (e != cudaSuccess || grid == 1) return e;
-  return launch_pdl(kv8_decode_join_kernel<D>, dim3(grid - 1), dim3(256), 0, s, p);
+  const int parts = TEAM ? grid : grid * warps_of(NT, W);
+  if (e != cudaSuccess || parts == 1) return e;
+  return launch_pdl(kv8_decode_join_kernel<D>, dim3(parts - 1), dim3(256), 0, s, p);
+}
+
+template <int D, int NT, int W>
+cudaError_t go_w(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, bool team, int grid, cudaStream_t s) {
+  return team ? go<D, NT, W, true>(km, vm, p, grid, s) : go<D, NT, W, false>(km, vm, p, grid, s);
 }
 
 template <int D>
-cudaError_t go_d(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, int grid, cudaStream_t s) {
+cudaError_t go_d(const CUtensorMap& km, const CUtensorMap& vm, const Kv8AttnParams& p, bool team, int grid, cudaStream_t s) {
   const bool two = p.T * p.G > 8;            // more than one product column block of 8 rows
-  if (p.dtype == TQ_F32) return two ? go<D, 2, 2>(km, vm, p, grid, s) : go<D, 1, 2>(km, vm, p, grid, s);
-  return two ? go<D, 2, 1>(km, vm, p, grid, s) : go<D, 1, 1>(km, vm, p, grid, s);
+  if (p.dtype == TQ_F32) return two ? go_w<D, 2, 2>(km, vm, p, team, grid, s) : go_w<D, 1, 2>(km, vm, p, team, grid, s);
+  return two ? go_w<D, 2, 1>(km, vm, p, team, grid, s) : go_w<D, 1, 1>(km, vm, p, team, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
-                              cudaStream_t s) {
-  return d == 128 ? go_d<128>(kmap, vmap, p, grid, s) : go_d<64>(kmap, vmap, p, grid, s);
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, bool team,
+                              int grid, cudaStream_t s) {
+  return d == 128 ? go_d<128>(kmap, vmap, p, team, grid, s) : go_d<64>(kmap, vmap, p, team, grid, s);
 }
 
 }  // namespace tq

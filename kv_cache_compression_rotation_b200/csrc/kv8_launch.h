@@ -63,8 +63,11 @@ struct Kv8AttnParams {
 constexpr int kKv8DecodeRows = 16;
 __host__ __device__ constexpr int kv8_decode_tile(int d) { return d == 64 ? 64 : 32; }       // tokens
 constexpr int kKv8DecodeMaxVB = 1024;                 // virtual sequences a launch
-cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, int grid,
-                              cudaStream_t s);
+// Warps of a CTA.  Their instructions' latency bounds a tile, so as many as the registers allow.
+__host__ __device__ constexpr int kv8_decode_warps(int64_t rows, bool f32) { return rows <= 8 && !f32 ? 12 : 8; }
+// team: the warps of a CTA share each run, else each has its own.
+cudaError_t launch_kv8_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const Kv8AttnParams& p, int d, bool team,
+                              int grid, cudaStream_t s);
 
 
 // Groups of 256 rows a key head, 16-bit queries (prefill).

@@ -888,7 +888,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         mbar_arrive(bar(DFULL + mb));
         if (run.tiles == 0) break;
       }
-      if (lane == 0) kv8_plan_split(p.plan, u0, u1, per, s_pref, VB, Hkv, run_cost(GEN));
+      if (lane == 0) kv8_plan_split(p.plan, blockIdx.x, u0, u1, per, s_pref, VB, Hkv, run_cost(GEN));
     }
   }
   tc_fence_before();
