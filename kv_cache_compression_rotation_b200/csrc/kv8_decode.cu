@@ -4,18 +4,23 @@
 //   l_t = scale q.k^_t (capped, biased),  out = sum_t softmax(l)_t v^_t,  lse = ln sum_t e^{l_t}
 //
 // Bytes bound it: each token of a key head is 2 d codes and 2 / 16 scales, read once for all its
-// query rows.  The launch has one CTA an SM; the tiles of 32 (d = 64: 64) tokens of all (sequence, key head)
-// pairs form one line that is cut into equal runs, one a CTA, so ragged lengths and few long
-// sequences load every SM alike.  A pair that one run covers is finished in the CTA; the others
-// leave at most two partial results a CTA, joined by a second, small kernel.
+// query rows (d = 128, eight sequences of 131072 tokens: 325 us, 6.6 TB/s).  Tiles of 8 KB of codes
+// (32 tokens at d = 128, 64 at d = 64) of all (sequence, key head) pairs form one line that is cut
+// into equal parts, so ragged lengths and few long sequences load every SM alike: a part for each
+// CTA, whose warps take its tiles in turn, or one for each warp (the rule stands in plan_attn).  A
+// pair that one part covers is finished there; the others leave at most two partial results a part,
+// joined by a second, small kernel.  In the line a pair has a few tiles' length more than its own,
+// for what a run costs beside them.
 //
-// Inside a CTA the warps work without meeting: each keeps its own ring of tiles, copied by the
-// tensor-map engine into swizzled rows (the swizzle frees the reads of the value operand from
-// bank conflicts) and takes every eighth or twelfth tile.  A tile's scores are S^T = K Q^T with 16 tokens as
-// the rows of an m16n8k16 product and eight query rows as its columns, so small groups of query
-// heads waste little of it; then O^T += V^T P^T with the dims as rows.  Codes become halves
-// (exact) on the way into the registers.  The order of the 16 dims of a step is free, as long as
-// q has it too: a lane reads 16 consecutive bytes of a row.
+// The warps work without meeting: each keeps its own ring of tiles, copied by the tensor-map engine
+// into swizzled rows (the swizzle frees the reads of the value operand from bank conflicts).  What
+// bounds a warp is the latency of its instructions, hence twelve where registers allow (eight: 400
+// us in place of 345 at 131072 tokens).  A tile's scores are S^T = K Q^T with 16 tokens as the rows
+// of an m16n8k16 product and eight query rows as its columns, so small groups of query heads waste
+// little of it (the tensor-memory instructions' 128 rows would be nine tenths empty); then
+// O^T += V^T P^T with the dims as rows.  Codes become halves (exact) on the way into the registers.
+// The order of the 16 dims of a step is free, as long as q has it too: a lane reads 16 consecutive
+// bytes of a row.
 //
 // Number ranges.  q is divided by a power of two a row so that its largest entry is in [1, 2) as
 // a half (entries below 2^-14 of it round to 2^-25 of it).  A value block's scale 2^e joins its

@@ -3,25 +3,35 @@
 //
 //   S = Q K^T,  l_t = scale s_k(t) S_t (capped, biased),  O = sum_t e^{l_t} v^_t,  out = O / sum
 //
-// 4 d operations a (row, token) and one exponential bound it: a tile pair of 2 x 128 rows and 128
-// tokens at d = 128 takes the tensor core 2048 cycles and the exponentials, 16 a cycle, as many.
+// 4 d operations a (row, token) and one exponential bound it: 2 x 128 rows and 128 tokens at d = 128
+// take the tensor core 2048 cycles and the exponentials, 16 a cycle, as many.  Measured: 4000 to 4300
+// cycles, of which a row tile's softmax is 2400 and its two products, which share the memory they
+// read with the conversion of the codes, 1500 (causal 8192 tokens, 32 heads: 558 us, 0.99 PFLOP/s;
+// two times 512 queries over 32768 tokens: 505 us, 1.08).
 //
 // A CTA an SM (persistent) takes runs of the line of (256-row group, key head, 128-token tile) as
-// the decode kernel does.  Its roles:
-//   warps 0-3, 4-7   softmax of row tile 0 and 1, a row a thread: scores from tensor memory,
-//                    running maximum and sum, probabilities back into tensor memory as halves
-//   warps 8-11       codes to halves: 16 bytes of codes become 32 of a 128-byte-swizzled operand
-//                    tile in shared memory; the next tile's codes are already in registers
-//   warp 12          the tensor core's issuing thread
+// the decode kernel does.  Its roles, with register shares of their own (setmaxnreg):
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, a row a thread: the scores of a tile are read from
+//                    tensor memory at once and stay in registers; running maximum and sum; the
+//                    probabilities go back into tensor memory as halves.  Between runs: q and results
+//   warps 8-11       codes to halves, in place: a tile's codes arrive in one half of its operand
+//                    tile and are expanded to all of it (128-byte swizzle)
+//   warp 12          issues the products
+//   warp 13          prepares runs: what their rows see
+//   warps 14, 15     ask for keys and scales, and for values (bulk copies of blocks, or of as many as
+//                    follow one another in the cache)
 // The two row tiles alternate: while one tile's scores are in the softmax, the tensor core works
-// for the other.  Tensor memory (512 columns): S 0, S 1 (128 each; the tile's probabilities
-// overwrite its scores, two a column), O 0, O 1.  K is a row-major operand, V the same bytes read
-// transposed.
+// for the other.  (A warp issuing for each row tile lets both fall into step: 606 us in place of 524.)
+// The second product begins with the first half of the probabilities (521 without, 512 with).  Tensor
+// memory (512 columns): S 0, S 1 (128 each; the tile's probabilities overwrite its scores, two a
+// column), O 0, O 1.  K is a row-major operand, V the same bytes read transposed.
 //
 // A row's reference stays while no score exceeds it by 2^8, so the outputs are seldom rescaled.
 // The value scales 2^e of 16-token blocks join the exponent: P = 2^(l - m + 7 + e - E), E the
-// largest e of the run, at most 2^15 in halves of 11 bits; row sums are fp32.  q is divided by a
-// power of two a row, as in the decode kernel.
+// largest e so far, at most 2^15 in halves of 11 bits (a probability below 2^-21 of the row's largest
+// loses bits to the halves' subnormal step, 2^-32 of it); row sums are fp32.  q is divided by a power
+// of two a row, as in the decode kernel.  A cap's tanh is a series where |score| <= cap / 2 for 512
+// scores at once, else exponential and division: both within 2^-20 of the cap.
 #include <cuda_runtime.h>
 
 #include "kv8_launch.h"
