@@ -144,6 +144,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t a, const float (&v)[32]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
+    tmem_st16(a + 16 * h, r);
+  }
+}
+
 // No use of v before this point (the wait for its load from tensor memory).
 __device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll
@@ -406,50 +416,75 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
           mbar_arrive(bar(KEMPTY + (kt & 1)));
           if (j > 0) mbar_arrive(bar(VEMPTY + ((kt - 1) & 1)));
         }
-        // the row's scores stay in registers (the probabilities overwrite them in tensor memory)
-        float s0[32], s1[32], s2[32], s3[32];
-        tmem_ld32(ts, s0);
-        tmem_ld32(ts + 32, s1);
         const float* sc = s_scale + (kt % kScaleSlots) * kSlot;
         const float E1 = sc[3 * kBlocks];
         const bool masked = __any_sync(0xffffffffu, t0 < lo || t0 + kTile > hi);
         const bool formed = GEN || masked;   // scores are formed here, else their scale joins the exponent
-        // Forms the scores of 32 tokens (their quarter: c), and their maximum.
-        auto top = [&](float (&s)[32], int c) {
-          if (formed) {
-            if (GEN && p.sc.cap > 0.f) {
-              const float by_cap = kLn2 / p.sc.cap * rowc, cap2 = p.sc.cap * kLog2E;
-              const float z0 = sc[2 * c] * by_cap, z1 = sc[2 * c + 1] * by_cap;
-              float far = 0.f, far1 = 0.f;
+        // Rolled, by way of tensor memory: copies of this for each 32 tokens cost the plain path its
+        // registers and its place in the instruction cache (561 us became 661).
+        if (formed) {
+#pragma unroll 1
+          for (int c = 0; c < kTile / 32; ++c) {
+            const int from = lo - t0 - 32 * c, to = hi - t0 - 32 * c;          // visible ones of the 32
+            const bool cut = masked && __any_sync(0xffffffffu, from > 0 || to < 32);
+            float s[32];
+            if (cut && __all_sync(0xffffffffu, from >= 32 || to <= 0)) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                far = fmaxf(far, fabsf(s[k]));
-                far1 = fmaxf(far1, fabsf(s[16 + k]));
-              }
-              if (__all_sync(0xffffffffu, fmaxf(far * z0, far1 * z1) <= 0.5f)) {
-                tanh_small(s, 0, z0, cap2);
-                tanh_small(s, 16, z1, cap2);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = cap2 * kv8_tanh(s[k] * (k < 16 ? z0 : z1));
-              }
+              for (int k = 0; k < 32; ++k) s[k] = -INFINITY;
             } else {
-              const float z0 = sc[2 * c] * rowc, z1 = sc[2 * c + 1] * rowc;
+              tmem_ld32(ts + 32 * c, s);
+              tmem_wait_ld();
+              pin(s);
+              if (GEN && p.sc.cap > 0.f) {
+                const float by_cap = kLn2 / p.sc.cap * rowc, cap2 = p.sc.cap * kLog2E;
+                const float z0 = sc[2 * c] * by_cap, z1 = sc[2 * c + 1] * by_cap;
+                float far = 0.f, far1 = 0.f;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] *= k < 16 ? z0 : z1;
-            }
-            if (GEN && p.sc.slopes) {
-              const float far0 = static_cast<float>(pos - t0 - 32 * c);
+                for (int k = 0; k < 16; ++k) {
+                  far = fmaxf(far, fabsf(s[k]));
+                  far1 = fmaxf(far1, fabsf(s[16 + k]));
+                }
+                if (__all_sync(0xffffffffu, fmaxf(far * z0, far1 * z1) <= 0.5f)) {
+                  tanh_small(s, 0, z0, cap2);
+                  tanh_small(s, 16, z1, cap2);
+                } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) s[k] = fmaf(-slope, fabsf(far0 - k), s[k]);
-            }
-            if (masked) {
-              const int a = lo - t0 - 32 * c, z = hi - t0 - 32 * c;
+                  for (int k = 0; k < 32; ++k) s[k] = cap2 * kv8_tanh(s[k] * (k < 16 ? z0 : z1));
+                }
+              } else {
+                const float z0 = sc[2 * c] * rowc, z1 = sc[2 * c + 1] * rowc;
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k < a || k >= z) s[k] = -INFINITY;
+                for (int k = 0; k < 32; ++k) s[k] *= k < 16 ? z0 : z1;
+              }
+              if (GEN && p.sc.slopes) {
+                const float far0 = static_cast<float>(pos - t0 - 32 * c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = fmaf(-slope, fabsf(far0 - k), s[k]);
+              }
+              if (cut) {
+                const uint32_t seen = (to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u) &
+                                      (from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(seen & (1u << k))) s[k] = -INFINITY;
+              }
             }
+            tmem_st32(ts + 32 * c, s);
           }
+          tmem_wait_st();
+        }
+        // the row's scores stay in registers (the probabilities overwrite them in tensor memory)
+        float s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(ts, s0);
+        tmem_ld32(ts + 32, s1);
+        tmem_ld32(ts + 64, s2);
+        tmem_ld32(ts + 96, s3);
+        tmem_wait_ld();
+        pin(s0);
+        pin(s1);
+        pin(s2);
+        pin(s3);
+        auto top = [&](const float (&s)[32], int c) {
           float a = s[0], b = s[16];
 #pragma unroll
           for (int k = 1; k < 16; ++k) {
@@ -458,13 +493,6 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
           }
           return formed ? fmaxf(a, b) : fmaxf(a * (sc[2 * c] * rowc), b * (sc[2 * c + 1] * rowc));
         };
-        tmem_ld32(ts + 64, s2);
-        tmem_ld32(ts + 96, s3);
-        tmem_wait_ld();
-        pin(s0);
-        pin(s1);
-        pin(s2);
-        pin(s3);
         const float mx = fmaxf(fmaxf(top(s0, 0), top(s1, 1)), fmaxf(top(s2, 2), top(s3, 3)));
         // ---- the reference, and what was summed against the old one and the old E
         const bool grow = mx > m + kLazy || m == -INFINITY;
