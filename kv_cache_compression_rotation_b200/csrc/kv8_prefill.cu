@@ -6,7 +6,7 @@
 // 4 d operations a (row, token) and one exponential bound it: 2 x 128 rows and 128 tokens at d = 128
 // take the tensor core 2048 cycles and the exponentials, 16 a cycle, as many.  Measured: 4000 to 4300
 // cycles, of which a row tile's softmax is 2400 and its two products, which share the memory they
-// read with the conversion of the codes, 1500 (causal 8192 tokens, 32 heads: 558 us, 0.99 PFLOP/s;
+// read with the conversion of the codes, 1500 (causal 8192 tokens, 32 heads: 537 us, 1.02 PFLOP/s;
 // two times 512 queries over 32768 tokens: 505 us, 1.08).
 //
 // A CTA an SM (persistent) takes runs of the line of (256-row group, key head, 128-token tile) as

@@ -608,6 +608,8 @@ class Kv8:
             raise ValueError("codes must be uint8 or float8_e4m3fn and scales float32")
         if codes.dim() != 2 or not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes [records, d] and scales must be contiguous")
+        if codes.device != scales.device:
+            raise ValueError(f"codes on {codes.device} and scales on {scales.device}")
         if scales.numel() * KV8_BLOCK != codes.shape[0]:
             raise ValueError(f"scales must hold one value for each {KV8_BLOCK} of the {codes.shape[0]} records")
         self.codes, self.scales, self.d, self.records = codes, scales, codes.shape[1], codes.shape[0]
@@ -634,16 +636,11 @@ class Scoring:
             if t is not None and (t.dtype is not dt or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous {dt} tensor")
         self.scale, self.slopes, self.first, self.prefix = scale, slopes, first, prefix
-        self.by_d = {}
         self.softcap, self.window = float(softcap), int(window)
 
     def as_c(self, d: int):
-        c = self.by_d.get(d)
-        if c is None:
-            c = Scoring_t(1.0 / math.sqrt(d) if self.scale is None else float(self.scale), self.softcap,
-                          _dptr(self.slopes), self.window, _dptr(self.first), _dptr(self.prefix))
-            self.by_d[d] = c
-        return c
+        return Scoring_t(1.0 / math.sqrt(d) if self.scale is None else float(self.scale), self.softcap,
+                         _dptr(self.slopes), self.window, _dptr(self.first), _dptr(self.prefix))
 
     def check(self, B: int, Hq: int, T: int) -> None:
         for name, t, n in (("slopes", self.slopes, Hq), ("first", self.first, B * T), ("prefix", self.prefix, B)):
@@ -684,6 +681,8 @@ def _kv8_cache(kcache: Kv8, vcache: Kv8, B: int, Hkv: int, Nmax: int, pages):
     if pages is not None:
         if pages.block_table.shape[0] < B or pages.block_table.element_size() != 4:
             raise ValueError(f"block_table must be int32 with a row for each of {B} sequences")
+        if pages.block_table.device != kcache.device:
+            raise ValueError(f"block_table on {pages.block_table.device}, the cache on {kcache.device}")
         return pages.max_pages * pages.page_size
     return Nmax
 
@@ -801,6 +800,8 @@ class PagePool:
             if t.dtype is not torch.int32 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor")
         self.block_table, self.refs, self.page_size, self.arrays = block_table, refs, page_size, list(arrays)
+        if refs.device != block_table.device:
+            raise ValueError(f"block_table on {block_table.device} and refs on {refs.device}")
         self.rows, self.max_pages = block_table.shape
         self.num_pages = refs.numel()
         self.device = block_table.device

@@ -255,3 +255,29 @@ def test_step_with_append_equals_append_then_step():
         for a, b in zip((kc, vc), other):
             assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
     assert K.get_status() == 0
+
+
+def test_tensors_on_another_device_are_refused():
+    """Nothing is launched for a table, scales, counts or lists on the host."""
+    q, pos, lens, kc, vc, pg = inputs(5300)
+    host = K.Pages(pg.block_table.cpu(), 16, pg.num_pages)
+    new = torch.zeros((2, 2, 1, 128), dtype=q.dtype, device="cuda")
+    for call in (lambda: K.kv8_prefill_attn(q, pos, lens, kc, vc, 2, pages=host),
+                 lambda: K.kv8_decode_attn(q[:, :, 0], lens, kc, vc, 2, pages=host),
+                 lambda: K.kv8_append(kc, vc, new, new, lens, pages=host),
+                 lambda: K.kv8_prefill_attn(q, pos.cpu(), lens, kc, vc, 2, pages=pg),
+                 lambda: K.kv8_prefill_attn(q, pos, lens, kc, vc, 2, pages=pg, scoring=K.Scoring(slopes=torch.zeros(8))),
+                 lambda: K.Kv8(kc.codes, kc.scales.cpu()),
+                 lambda: K.PagePool(pg.block_table, torch.zeros(50, dtype=torch.int32), 16),
+                 lambda: K.PagePool(pg.block_table, torch.zeros(pg.num_pages, dtype=torch.int32, device="cuda"), 16, [kc.codes.cpu()])):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_options_that_change_between_calls_count():
+    q, pos, lens, kc, vc, pg = inputs(5400)
+    sc = K.Scoring(window=50)
+    run = lambda s: K.kv8_prefill_attn(q, pos, lens, kc, vc, 2, pages=pg, scoring=s)
+    a = run(sc)
+    sc.window, sc.slopes = 0, torch.full((8,), 0.25, device="cuda")
+    assert torch.equal(run(sc), run(K.Scoring(slopes=sc.slopes))) and not torch.equal(run(sc), a)
