@@ -904,6 +904,7 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
         if (lt == 0) meta.run = run;
         if (run.tiles > 0) {
           const int b = run.b;
+#pragma unroll 2
           for (int rr = lt; rr < kKv8PrefillRows; rr += kScouts) {
             const int r = run.r0 + rr;
             int lo = 0, hi = INT32_MAX, pos = 0;
