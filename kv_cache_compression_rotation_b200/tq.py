@@ -204,9 +204,14 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _dtype_code(t) -> int:
+@functools.lru_cache(maxsize=None)
+def _dtype_codes() -> dict:
     import torch
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[t.dtype]
+    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _dtype_code(t) -> int:
+    return _dtype_codes()[t.dtype]
 
 
 def version() -> str:
@@ -707,7 +712,7 @@ def kv8_append(kcache: Kv8, vcache: Kv8, k_new, v_new, kv_lens, new_lens=None, N
 def kv8_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, T: int, d: int, Nmax: int) -> int:
     """Workspace of the 8-bit attention calls (T = 1: decode); dtype as a torch dtype."""
     import torch
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
+    code = _dtype_codes()[dtype]
     return _kv8_ws_bytes(torch.cuda.current_device() if torch.cuda.is_initialized() else -1, code, B, Hq, Hkv, T, d, Nmax)
 
 
@@ -745,7 +750,7 @@ def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 
                 k_new.dtype is not q.dtype or v_new.dtype is not q.dtype:
             raise ValueError(f"k_new and v_new must be [{B}, {Hkv}, {d}] of q's dtype")
         kst, vst = (C.byref(Strides_t(t.stride(0), t.stride(1), 0)) for t in (k_new, v_new))
-    out, lse, ws = _kv8_outputs(q, (B, Hq, d), out, lse, return_lse, workspace, B, Hq, Hkv, 1, d, cap)
+    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, d), out, lse, return_lse, workspace, B, Hq, Hkv, 1, d, cap)
     _check(lib().tq_kv8_decode_attn(_rows(q, "q", d), C.byref(Strides_t(q.stride(0), q.stride(1), 0)), _dtype_code(q), B,
                                     Hq, Hkv, d, _ints(kv_lens, B, "kv_lens"), C.byref(scoring.as_c(d)),
                                     None if pages is None else pages.ref, Nmax,
@@ -755,14 +760,14 @@ def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 
     return (out, lse) if return_lse else out
 
 
-def _kv8_outputs(q, shape, out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap):
+def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap):
     import torch
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if out is None:                            # (new_empty costs the host a third less than empty)
+        out = q.new_empty(shape)
     elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(shape)}")
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+        lse = kcache.scales.new_empty(shape[:-1]) if return_lse else None
     elif lse.shape != shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape[:-1])}")
     if workspace is None:
@@ -779,7 +784,7 @@ def kv8_prefill_attn(q, q_pos, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax
     cap, scoring = _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring)
     _same_device(q.device, q_pos, kv_lens, kcache.codes, vcache.codes, out, lse, workspace, scoring.slopes,
                  scoring.first, scoring.prefix)
-    out, lse, ws = _kv8_outputs(q, (B, Hq, T, d), out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap)
+    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, T, d), out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap)
     st = q.stride()
     _check(lib().tq_kv8_prefill_attn(_rows(q, "q", d), C.byref(Strides_t(st[0], st[1], st[2])), _dtype_code(q), B, Hq, Hkv,
                                      T, d, _ints(q_pos, B * T, "q_pos"), _ints(kv_lens, B, "kv_lens"),
@@ -833,8 +838,7 @@ class PagePool:
 
 
 def _one_int(pool: PagePool):
-    import torch
-    return torch.empty(1, dtype=torch.int32, device=pool.device)
+    return pool.refs.new_empty(1)
 
 
 def pages_free(pool: PagePool, rows, lens, stream=None) -> None:
@@ -873,9 +877,8 @@ def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, s
 def pages_compact(pool: PagePool, page_map=None, live=None, workspace=None, stream=None):
     """tq_pages_compact: live pages move to the lowest ids.  Returns page_map int32 [num_pages] (new
     id of each page, -1: free); live int32 [1], where given, receives their number."""
-    import torch
     _same_device(pool.device, page_map, live, workspace)
-    page_map = torch.empty(pool.num_pages, dtype=torch.int32, device=pool.device) if page_map is None else page_map
+    page_map = pool.refs.new_empty(pool.num_pages) if page_map is None else page_map
     live = _one_int(pool) if live is None else live
     ws = pool._work(0) if workspace is None else workspace
     _check(lib().tq_pages_compact(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(page_map, pool.num_pages, "page_map"),
