@@ -691,8 +691,14 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Kv8AttnParam
 #pragma unroll
     for (int k = 0; k < PL; ++k) o[k] = 0.f;
     auto slot_of = [&](int c) { return c * 2 + (c == c0 ? 1 : 0); };
-    for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.part_lse + slot_of(c) * kKv8DecodeRows + rl));
+    bool bad = false;                          // a NaN among the scores stays one
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float x = __ldcg(p.part_lse + slot_of(c) * kKv8DecodeRows + rl);
+      bad |= x != x;
+      mx = fmaxf(mx, x);
+    }
     mx = warp_max(mx);
+    bad = __any_sync(0xffffffffu, bad);
     if (mx > -INFINITY) {
 #pragma unroll 4
       for (int c = c0; c <= c1; ++c) {
@@ -704,8 +710,8 @@ __global__ void __launch_bounds__(256) kv8_decode_join_kernel(const Kv8AttnParam
         for (int k = 0; k < PL; ++k) o[k] += w * __ldcg(src + k);
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+    const float inv = bad ? NAN : sum > 0.f ? 1.f / sum : 0.f;
+    if (p.lse && lane == 0) p.lse[row] = bad ? NAN : sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
     const int64_t at = row * D + lane * PL;
 #pragma unroll
     for (int k = 0; k < PL; ++k) {

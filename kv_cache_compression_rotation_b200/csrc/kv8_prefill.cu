@@ -959,8 +959,14 @@ __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const Kv8AttnPara
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.f;
   auto prow = [&](int c) { return static_cast<int64_t>(c * 2 + (c == c0 ? 1 : 0)) * kKv8PrefillRows + rl; };
-  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(p.part_lse + prow(c)));
+  bool bad = false;                          // a NaN among the scores stays one
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float x = __ldcg(p.part_lse + prow(c));
+    bad |= x != x;
+    mx = fmaxf(mx, x);
+  }
   mx = warp_max(mx);
+  bad = __any_sync(0xffffffffu, bad);
   if (mx > -INFINITY)
     for (int c = c0; c <= c1; ++c) {
       const float w = ex2(__ldcg(p.part_lse + prow(c)) - mx);
@@ -969,8 +975,8 @@ __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const Kv8AttnPara
 #pragma unroll
       for (int k = 0; k < PL; ++k) o[k] += w * __ldcg(src + k);
     }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  const float inv = bad ? NAN : sum > 0.f ? 1.f / sum : 0.f;
+  if (p.lse && lane == 0) p.lse[row] = bad ? NAN : sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
 #pragma unroll
   for (int k = 0; k < PL; ++k) {
     const float x = o[k] * inv;

@@ -281,3 +281,34 @@ def test_options_that_change_between_calls_count():
     a = run(sc)
     sc.window, sc.slopes = 0, torch.full((8,), 0.25, device="cuda")
     assert torch.equal(run(sc), run(K.Scoring(slopes=sc.slopes))) and not torch.equal(run(sc), a)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [
+    dict(B=1, Hq=4, Hkv=1, lens=[20000], page=64, T=25),                 # 100 rows a key head over many blocks of threads
+    dict(B=3, Hq=2, Hkv=2, lens=[9001, 128, 4700], page=16, T=64, dtype="f16"),
+    dict(B=2, Hq=8, Hkv=2, lens=[3000, 2999], page=0, T=32, cap=4.0, window=900, docs=True),
+    dict(B=1, Hq=3, Hkv=1, lens=[130], page=16, T=40, alibi=True),
+    dict(B=5, Hq=4, Hkv=1, lens=[700, 129, 257, 1025, 40], page=48, T=20),
+], ids=["long", "ragged", "capped", "short", "mixed"])
+def test_few_rows_over_long_sequences(kw, d):
+    """One row tile a run, in many parts."""
+    kw = {"dtype": "bf16", **kw}
+    case(6000 + d, d=d, **kw)
+
+
+@pytest.mark.parametrize("T", [1, 30, 100])
+@pytest.mark.parametrize("n", [60, 6000])
+def test_nan_in_a_query_stays_in_its_row(T, n):
+    """A NaN query gives NaN (results joined from several parts too); the other rows keep their bits."""
+    q, pos, lens, kc, vc, pg = inputs(6100 + n + T, n=n + 100, T=T)
+    run = lambda x: K.kv8_prefill_attn(x, pos, lens, kc, vc, 2, pages=pg, return_lse=True)
+    want = run(q)
+    bad = q.clone()
+    bad[1, 5, T // 2, 17] = float("nan")
+    out, lse = run(bad)
+    assert out[1, 5, T // 2].isnan().all() and lse[1, 5, T // 2].isnan()
+    keep = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+    keep[1, 5, T // 2] = False
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+    assert K.get_status() == 0
