@@ -466,6 +466,14 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
       if (m <= -2) m = p.to[-2 - m];
       if (m != id) p.pool.block_table[e] = m;
     }
+    // counts and map of the pages that move, whether or not the pool has arrays
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; j < pairs;
+         j += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int from = p.from[j], to = p.to[j];
+      p.pool.refs[to] = p.pool.refs[from];
+      p.pool.refs[from] = 0;
+      *static_cast<volatile int32_t*>(p.page_map + from) = to;
+    }
   }
   const int slices = p.copy.slice0[p.copy.n];
   for (int64_t w = blockIdx.x; w < pairs * slices; w += gridDim.x) {
@@ -479,11 +487,6 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
       if (threadIdx.x == 0) report_status(p.status, TQ_ERR_INVALID_ARG);
       continue;
     }
-    if (MODE == COPY_COMPACT && s == 0 && threadIdx.x == 0) {
-      p.pool.refs[to] = p.pool.refs[from];
-      p.pool.refs[from] = 0;
-      *static_cast<volatile int32_t*>(p.page_map + from) = to;
-    }
     if (from == to) continue;
     int a = 0;
     while (s >= p.copy.slice0[a + 1]) ++a;
@@ -496,9 +499,10 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
   }
 }
 
-// Blocks of a copy: all slices where they are few, else eight an SM.
+// Blocks of a copy: all slices (or rounds of the lists, where there are no arrays) where they are few,
+// else eight an SM.
 unsigned copy_grid(int64_t pairs, const PagesParams& p, int sms) {
-  const int64_t all = pairs * p.copy.slice0[p.copy.n];
+  const int64_t all = std::max<int64_t>(pairs * p.copy.slice0[p.copy.n], (pairs + kThreads - 1) / kThreads);
   return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(all, 8ll * sms)));
 }
 

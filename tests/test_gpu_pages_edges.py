@@ -1,0 +1,63 @@
+"""GPU tests of the page pool's calls at their edges: pools without arrays, in the form of one block and
+the form of many, against the oracle (whole numbers, all equal)."""
+import numpy as np
+import pytest
+
+from oracle import kv8 as O
+
+import _kv8 as H
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+K = pytest.importorskip("kv_cache_compression_rotation_b200")
+
+i32 = lambda x: torch.tensor(list(x), dtype=torch.int32, device="cuda")
+dev = lambda a: torch.from_numpy(a.astype(np.int32)).cuda()
+
+
+@pytest.mark.parametrize("rows,mp,page,pages", [(6, 5, 16, 23), (40, 9, 16, 300), (60, 300, 16, 16384), (80, 300, 16, 20011)])
+def test_pool_without_arrays(rows, mp, page, pages):
+    """Counts, entries, map and number of live pages are those of a pool with arrays."""
+    r = H.rng(rows + pages)
+    table, refs, lens = np.full((rows, mp), -1), np.zeros(pages, int), [0] * rows
+    d_table, d_refs = dev(table), dev(refs)
+    pool = K.PagePool(d_table, d_refs, page)
+
+    def check():
+        assert np.array_equal(d_table.cpu().numpy(), table) and np.array_equal(d_refs.cpu().numpy(), refs)
+
+    for step in range(6):
+        grow = [i for i in range(rows) if lens[i] == 0 and r.random() < 0.7]
+        new = [int(r.integers(1, mp * page + 1)) for _ in grow]
+        if grow:
+            want = O.pool_reserve(table, refs, grow, [0] * len(grow), new, page)
+            assert K.pages_reserve(pool, i32(grow), i32([0] * len(grow)), i32(new)).item() == want
+            if want == 0:
+                for i, n in zip(grow, new):
+                    lens[i] = n
+            check()
+        held = [i for i in range(rows) if lens[i]]
+        dst = [i for i in range(rows) if not lens[i]][:5]
+        if held and dst:
+            src = [held[int(r.integers(len(held)))] for _ in dst]
+            ln = [lens[i] for i in src]
+            want = O.pool_fork(table, refs, [], src, dst, ln, page)
+            assert K.pages_fork(pool, i32(src), i32(dst), i32(ln)).item() == want
+            if want == 0:
+                for i, n in zip(dst, ln):
+                    lens[i] = n
+            check()
+        gone = [i for i in range(rows) if lens[i] and r.random() < 0.5]
+        if gone:
+            ln = [lens[i] for i in gone]
+            O.pool_free(table, refs, gone, ln, page)
+            K.pages_free(pool, i32(gone), i32(ln))
+            for i in gone:
+                lens[i] = 0
+        page_map, n = O.pool_compact(table, refs, [])
+        live = i32([0])
+        got = K.pages_compact(pool, live=live)
+        assert np.array_equal(got.cpu().numpy(), page_map) and live.item() == n
+        check()
+    assert K.get_status() == 0
