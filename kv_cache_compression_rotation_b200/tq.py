@@ -1,13 +1,15 @@
 """ctypes binding of libtq (include/tq.h): argument marshalling only.
 
 Every computation runs in the CUDA library; PyTorch supplies device memory and the
-current stream.  If ``libtq.so`` is missing the first call raises -- there is no CPU
+current stream.  With ``stream=`` a call runs on that stream, which also owns what the call
+allocates; its inputs must be ready there and live until it is done with them.  If ``libtq.so`` is missing the first call raises -- there is no CPU
 fallback.  Build it with ``python -m kv_cache_compression_rotation_b200.build``.
 """
 from __future__ import annotations
 
 import ctypes as C
 import functools
+import inspect
 import math
 import os
 from dataclasses import dataclass
@@ -204,6 +206,38 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _tensors(x):
+    """The tensors of what a call returns."""
+    if isinstance(x, (tuple, list)):
+        return [t for y in x for t in _tensors(y)]
+    if isinstance(x, Packed):
+        return [t for t in (x.codes, x.signs, x.norms, x.rnorms) if t is not None]
+    return [x] if hasattr(x, "record_stream") else []
+
+
+def _on_stream(f):
+    """For calls that allocate.  With stream= they run as if it were the current stream, so that what
+    they allocate belongs to it: a workspace that is dropped at return goes to nobody else while the
+    kernels use it, and an output's memory to nobody while the caller's stream reads it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        import torch
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            result = f(*args, **kw)
+        if here != stream:
+            for t in _tensors(result):
+                t.record_stream(here)
+        return result
+
+    return call
+
+
 @functools.lru_cache(maxsize=None)
 def _dtype_codes() -> dict:
     import torch
@@ -397,6 +431,7 @@ class Quantizer:
 
 
 # ------------------------------------------------------------------ device calls
+@_on_stream
 def quantize(q: Quantizer, x, out: Optional[Packed] = None, stream=None) -> Packed:
     """tq_quantize_{mse,prod,spectral} of x [n, d] (fp32 / bf16 / fp16 CUDA tensor)."""
     assert x.is_cuda and x.is_contiguous() and x.shape[-1] == q.d
@@ -414,6 +449,7 @@ def tq_quantize_workspace_bytes(q: Quantizer, x) -> int:
     return ws.value
 
 
+@_on_stream
 def quantize_ws(q: Quantizer, x, out: Optional[Packed] = None, workspace=None, stream=None) -> Packed:
     """tq_quantize_ws: the same records as quantize(), with device scratch (wide fp32 vectors
     take the tensor-core split-precision path)."""
@@ -430,6 +466,7 @@ def quantize_ws(q: Quantizer, x, out: Optional[Packed] = None, workspace=None, s
     return out
 
 
+@_on_stream
 def dequantize(q: Quantizer, packed: Packed, n: int, stream=None):
     import torch
     out = torch.empty((n, q.d), dtype=torch.float32, device=packed.codes.device)
@@ -437,6 +474,7 @@ def dequantize(q: Quantizer, packed: Packed, n: int, stream=None):
     return out
 
 
+@_on_stream
 def score(q: Quantizer, qv, packed: Packed, n: int, topk: int = 0, stream=None):
     """Dense estimates [nq, n], or (scores [nq, topk], ids [nq, topk]) when topk > 0."""
     import torch
@@ -478,6 +516,7 @@ def _packed_array(packs):
     return (Packed_t * len(packs))(*[p.as_c() for p in packs])
 
 
+@_on_stream
 def quantize_split(sp: Split, x, out=None, stream=None):
     """tq_quantize_split of x [n, d]: one list entry of packed records per group."""
     assert x.is_cuda and x.is_contiguous() and x.shape[-1] == sp.d
@@ -487,6 +526,7 @@ def quantize_split(sp: Split, x, out=None, stream=None):
     return out
 
 
+@_on_stream
 def score_split(sp: Split, qv, packs, n: int, topk: int = 0, stream=None):
     """Summed split estimates [nq, n], or (scores, ids) of the top-k when topk > 0."""
     import torch
@@ -505,6 +545,7 @@ def score_split(sp: Split, qv, packs, n: int, topk: int = 0, stream=None):
     return scores if topk == 0 else (scores, ids)
 
 
+@_on_stream
 def decode_attn_split(ks: Split, vs: Split, q, seq_lens, kpacks, vpacks, Nmax: int, Hkv: int, scale=None,
                       out=None, stream=None):
     """tq_decode_attn_split for q [B, Hq, d] over split caches (one packed list per split)."""
@@ -528,6 +569,7 @@ def decode_workspace_bytes(kq: Quantizer, B: int, Hq: int, Hkv: int, Nmax: int) 
     return ws.value
 
 
+@_on_stream
 def decode_attn(kq: Quantizer, vq: Quantizer, q, seq_lens, kcache: Packed, vcache: Packed, Nmax: int,
                 Hkv: int, scale: Optional[float] = None, out=None, workspace=None, stream=None):
     """One decode-attention step; q [B, Hq, d], seq_lens int32 [B] on the device."""
@@ -563,6 +605,7 @@ class Pages:
         return self.num_pages * Hkv * self.page_size
 
 
+@_on_stream
 def decode_attn_paged(kq: Quantizer, vq: Quantizer, q, seq_lens, pages: Pages, kpool: Packed, vpool: Packed,
                       Hkv: int, k_new=None, v_new=None, scale: Optional[float] = None, out=None, workspace=None,
                       stream=None):
@@ -581,6 +624,7 @@ def decode_attn_paged(kq: Quantizer, vq: Quantizer, q, seq_lens, pages: Pages, k
     return out
 
 
+@_on_stream
 def prefill_attn(kq: Quantizer, vq: Quantizer, q, q_pos, kv_lens, kcache: Packed, vcache: Packed, Hkv: int,
                  Nmax: int = 0, pages: Optional[Pages] = None, scale: Optional[float] = None, out=None,
                  workspace=None, stream=None):
@@ -735,6 +779,7 @@ def _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring):
     return cap, scoring
 
 
+@_on_stream
 def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0, pages: Optional[Pages] = None,
                     k_new=None, v_new=None, scoring: Optional[Scoring] = None, out=None, lse=None,
                     return_lse: bool = False, workspace=None, stream=None):
@@ -775,6 +820,7 @@ def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, B, Hq, Hkv, 
     return out, lse, workspace
 
 
+@_on_stream
 def kv8_prefill_attn(q, q_pos, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0,
                      pages: Optional[Pages] = None, scoring: Optional[Scoring] = None, out=None, lse=None,
                      return_lse: bool = False, workspace=None, stream=None):
@@ -848,6 +894,7 @@ def pages_free(pool: PagePool, rows, lens, stream=None) -> None:
     _check(lib().tq_pages_free(C.byref(pool.c), _ints(rows, n, "rows"), _ints(lens, n, "lens"), n, _stream(stream)))
 
 
+@_on_stream
 def pages_reserve(pool: PagePool, rows, old_lens, new_lens, shortfall=None, workspace=None, stream=None):
     """tq_pages_reserve: rows int32 [n] grow from old_lens to new_lens tokens.  Returns the device
     int32 [1] shortfall (0 = done)."""
@@ -861,6 +908,7 @@ def pages_reserve(pool: PagePool, rows, old_lens, new_lens, shortfall=None, work
     return shortfall
 
 
+@_on_stream
 def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, stream=None):
     """tq_pages_fork: row dst[i] continues from the first lens[i] tokens of row src[i] (int32 [n]
     each).  Returns the device int32 [1] shortfall (0 = done)."""
@@ -874,6 +922,7 @@ def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, s
     return shortfall
 
 
+@_on_stream
 def pages_compact(pool: PagePool, page_map=None, live=None, workspace=None, stream=None):
     """tq_pages_compact: live pages move to the lowest ids.  Returns page_map int32 [num_pages] (new
     id of each page, -1: free); live int32 [1], where given, receives their number."""
