@@ -80,9 +80,54 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh from 1 - 2 / (1 + e^2x): absolute error near 2^-22, which the cap scales.
+// Two floats an instruction.
+__device__ __forceinline__ float2 pair(float x, float y) { return make_float2(x, y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+
+// tanh from 1 - 2 / (1 + e^2x): absolute error near 2^-22.
 __device__ __forceinline__ float kv8_tanh(float x) {
   return 1.f - __fdividef(2.f, 1.f + ex2(fminf(x * (2.f * kLog2E), 80.f)));
+}
+
+// Capped scores, out * tanh(z).  A cap may be far above the scores, so the error is kept relative: for
+// |z| <= 1/2 the series to z^11, whose next term is below 2^-20 of the result, else kv8_tanh of |z|.
+__device__ __forceinline__ float2 kv8_cap_series(float2 z, float out) {
+  const float2 u = mul2(z, z), y = mul2(z, both(out));
+  float2 q = fma2(u, both(-1382.f / 155925.f), both(62.f / 2835.f));
+  q = fma2(u, q, both(-17.f / 315.f));
+  q = fma2(u, q, both(2.f / 15.f));
+  q = fma2(u, q, both(-1.f / 3.f));
+  return fma2(mul2(y, u), q, y);
+}
+__device__ __forceinline__ float2 kv8_cap(float2 z, float out) {
+  const float2 near = kv8_cap_series(z, out);
+  return make_float2(fabsf(z.x) <= 0.5f ? near.x : copysignf(out * kv8_tanh(fabsf(z.x)), z.x),
+                     fabsf(z.y) <= 0.5f ? near.y : copysignf(out * kv8_tanh(fabsf(z.y)), z.y));
 }
 
 // Two e4m3 codes (low 16 bits) as two halves; every e4m3 value is exact in half precision.

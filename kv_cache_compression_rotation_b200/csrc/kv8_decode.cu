@@ -412,19 +412,52 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           }
         }
       }
+      // Capped ones: most are below half the cap, and where all are the series alone does (the same bits either way).
+      if (p.sc.cap > 0.f) {
+        const float in = kLn2 / p.sc.cap, out = p.sc.cap * kLog2E;
+        float far = 0.f;
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float2 z = mul2(mul2(pair(s[bl][nt][k], s[bl][nt][k + 1]), pair(ksc[bl] * cs[nt][0], ksc[bl] * cs[nt][1])), both(in));
+              s[bl][nt][k] = z.x;
+              s[bl][nt][k + 1] = z.y;
+              far = fmaxf(far, fmaxf(fabsf(z.x), fabsf(z.y)));
+            }
+        const bool near = __all_sync(0xffffffffu, far <= 0.5f);
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float2 z = pair(s[bl][nt][k], s[bl][nt][k + 1]);
+              const float2 y = near ? kv8_cap_series(z, out) : kv8_cap(z, out);
+              s[bl][nt][k] = y.x;
+              s[bl][nt][k + 1] = y.y;
+            }
+      } else {
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[bl][nt][k] *= ksc[bl] * cs[nt][k & 1];
+      }
       float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
       for (int bl = 0; bl < NB; ++bl) {
-        const float kscale = ksc[bl];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int c = k & 1, t = t0 + bl * 16 + g + (k >> 1) * 8;
-            float x = s[bl][nt][k] * (kscale * cs[nt][c]);
-            if (p.sc.cap > 0.f) x = p.sc.cap * kLog2E * kv8_tanh(x * (kLn2 / p.sc.cap));
+            float x = s[bl][nt][k];
             if (p.sc.slopes) x -= slope[nt][c] * static_cast<float>(abs(pos[nt][c] - t));
             if (masked && (t < lo[nt][c] || t >= hi[nt][c])) x = -INFINITY;
             s[bl][nt][k] = x;

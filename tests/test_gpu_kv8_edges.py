@@ -1,0 +1,81 @@
+"""GPU tests of the 8-bit attention at the edges of what its calls accept, against the float64 oracle's
+formulas in matrix form.
+
+Bounds (nats), before the output's own rounding: a score 2^-19 scale sum|q k| + 2^-20 |s|, a capped one
+2^-19 |s| more (three roundings of its factors, a series cut at 2^-20 of the result or an exponential and a
+division, each within 2^-22 of 1, where tanh is above 0.46), 2^-20 (1 + distance from the largest) for the
+exponential; the output P_EPS + the score's error + their mean + n 2^-27, each times sum p |v|."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import kv8 as O
+
+import _kv8 as H
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+K = pytest.importorskip("kv_cache_compression_rotation_b200")
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+HALF_STEP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+TINY = {"bf16": 2.0 ** -133, "f16": 2.0 ** -25, "f32": 2.0 ** -149}
+P_EPS = {"bf16": 2.0 ** -11, "f16": 2.0 ** -11, "f32": 2.0 ** -21}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def side(codes, scales):
+    return K.Kv8(dev(codes), dev(scales))
+
+
+def attend(q, pos, lens, kc, vc, Hkv, cap_tokens, **kw):
+    """The decode call for one query a sequence, else the call for blocks of queries."""
+    if q.shape[2] == 1:
+        o, l = K.kv8_decode_attn(q[:, :, 0], lens, kc, vc, Hkv, Nmax=cap_tokens, return_lse=True, **kw)
+        return o[:, :, None], l[:, :, None]
+    return K.kv8_prefill_attn(q, pos, lens, kc, vc, Hkv, Nmax=cap_tokens, return_lse=True, **kw)
+
+
+def setup(seed, T, d, dtype, n=300, Hq=4, Hkv=2, q_spread=1.0):
+    """One sequence of n tokens whose last T are the queries."""
+    r = H.rng(seed)
+    lay = H.Layout(r, 1, Hkv, n, 0)
+    data = [H.random_side(r, lay.records, d) for _ in range(2)]
+    qt = torch.from_numpy(r.standard_normal((1, Hq, T, d)).astype(np.float32) * np.float32(q_spread)).to(DT[dtype])
+    pos = np.arange(n - T, n, dtype=np.int32)[None]
+    return lay, data, qt, pos, dev(np.array([n], np.int32))
+
+
+@pytest.mark.parametrize("cap", [0.5, 6.0, 50.0, 1e3, 1e6, 1e30])
+@pytest.mark.parametrize("T,d,dtype", [(1, 128, "bf16"), (1, 64, "f32"), (3, 64, "f16"), (60, 128, "f16"), (60, 64, "bf16"), (40, 128, "f32")])
+def test_caps_of_any_size(T, d, dtype, cap):
+    lay, data, qt, pos, lens = setup(100 + T + d, T, d, dtype, q_spread=2.0)
+    kc, vc = (side(c, s) for c, s in data)
+    out, lse = attend(qt.cuda(), dev(pos), lens, kc, vc, 2, lay.cap, scoring=K.Scoring(softcap=cap))
+    assert K.get_status() == 0
+    out, lse, q64 = out.double().cpu().numpy(), lse.double().cpu().numpy(), qt.double().numpy()
+    values, n, scale = [H.values(c, s) for c, s in data], 300, d ** -0.5
+    see = np.arange(n) <= pos[0][:, None]
+    for hq in range(4):
+        rec = lay.rec(0, hq // 2, n)
+        k, v = (x[rec] for x in values)
+        s = cap * np.tanh(scale * (q64[0, hq] @ k.T) / cap)
+        mag = scale * (np.abs(q64[0, hq]) @ np.abs(k).T)
+        s = np.where(see, s, -np.inf)
+        m = s.max(1, keepdims=True)
+        e = np.exp(s - m)
+        w = e / e.sum(1, keepdims=True)
+        fin = np.where(see, s, m)
+        err = np.where(see, 2.0 ** -19 * mag + (2.0 ** -20 + 2.0 ** -19) * np.abs(fin) + 2.0 ** -20 * (1 + (m - fin).clip(0, 200)), 0)
+        mean = (w * err).sum(1, keepdims=True)
+        ob = (w * (P_EPS[dtype] + err + mean + n * 2.0 ** -27)) @ np.abs(v)
+        want = w @ v
+        tol = ob + HALF_STEP[dtype] * (np.abs(want) + ob) + TINY[dtype]
+        assert np.all(np.abs(out[0, hq] - want) <= tol), float(np.max(np.abs(out[0, hq] - want) / tol))
+        l = m[:, 0] + np.log(e.sum(1))
+        assert np.all(np.abs(lse[0, hq] - l) <= mean[:, 0] + 2.0 ** -20 + 2.0 ** -23 * np.abs(l))
