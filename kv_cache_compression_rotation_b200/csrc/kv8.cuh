@@ -109,9 +109,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return floats2(r);
 }
 
-// tanh from 1 - 2 / (1 + e^2x): absolute error near 2^-22.
+// tanh from 1 - 2 / (1 + e^2x): absolute error near 2^-22.  A NaN stays one.
 __device__ __forceinline__ float kv8_tanh(float x) {
-  return 1.f - __fdividef(2.f, 1.f + ex2(fminf(x * (2.f * kLog2E), 80.f)));
+  float e;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(x * (2.f * kLog2E)), "f"(80.f));
+  return 1.f - __fdividef(2.f, 1.f + ex2(e));
 }
 
 // Capped scores, out * tanh(z).  A cap may be far above the scores, so the error is kept relative: for

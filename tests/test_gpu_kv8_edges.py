@@ -79,3 +79,28 @@ def test_caps_of_any_size(T, d, dtype, cap):
         assert np.all(np.abs(out[0, hq] - want) <= tol), float(np.max(np.abs(out[0, hq] - want) / tol))
         l = m[:, 0] + np.log(e.sum(1))
         assert np.all(np.abs(lse[0, hq] - l) <= mean[:, 0] + 2.0 ** -20 + 2.0 ** -23 * np.abs(l))
+
+
+@pytest.mark.parametrize("cap", [0.01, 4.0, 1e4])
+@pytest.mark.parametrize("T,dtype", [(1, "bf16"), (3, "f32"), (30, "f16"), (100, "bf16"), (30, "f32")])
+def test_nan_under_a_cap_stays_nan(T, dtype, cap):
+    """A NaN in a query gives NaN in its row and nowhere else, whether its neighbours' scores are small or
+    large against the cap; a NaN key gives NaN to the rows that see it."""
+    lay, data, qt, pos, lens = setup(200 + T, T, 128, dtype)
+    kc, vc = (side(c, s) for c, s in data)
+    run = lambda x, k=kc: attend(x, dev(pos), lens, k, vc, 2, lay.cap, scoring=K.Scoring(softcap=cap))
+    q = qt.cuda()
+    want = run(q)
+    bad = q.clone()
+    bad[0, 2, T // 2, 17] = float("nan")
+    out, lse = run(bad)
+    assert out[0, 2, T // 2].isnan().all() and lse[0, 2, T // 2].isnan()
+    keep = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+    keep[0, 2, T // 2] = False
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+    codes = data[0][0].copy()
+    codes[lay.rec(0, 1, 300)[299]] = 0x7f                 # the last token of key head 1: the last query sees it
+    out, lse = run(q, side(codes, data[0][1]))
+    assert out[0, 2:, T - 1].isnan().all() and lse[0, 2:, T - 1].isnan().all()
+    assert not out[0, :2].isnan().any() and not out[0, :, :T - 1].isnan().any()
+    assert K.get_status() == 0
