@@ -30,8 +30,9 @@
 // The value scales 2^e of 16-token blocks join the exponent: P = 2^(l - m + 7 + e - E), E the
 // largest e so far, at most 2^15 in halves of 11 bits (a probability below 2^-21 of the row's largest
 // loses bits to the halves' subnormal step, 2^-32 of it); row sums are fp32.  q is divided by a power
-// of two a row, as in the decode kernel.  A cap's tanh is a series where |score| <= cap / 2 for 512
-// scores at once, else exponential and division: both within 2^-20 of the cap.
+// of two a row, as in the decode kernel.  A capped score is a series where it is at most cap / 2, else
+// exponential and division (kv8_cap); where 1024 of them are small at once, the series alone.  So a row's
+// bits do not depend on its neighbours' scores, or on those that a mask hides.
 #include <cuda_runtime.h>
 
 #include "kv8_launch.h"
@@ -420,7 +421,11 @@ kv8_prefill_kernel(const uint8_t* __restrict__ kcodes, const uint8_t* __restrict
                   tanh_small(s, 16, z1, cap2);
                 } else {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) s[k] = cap2 * kv8_tanh(s[k] * (k < 16 ? z0 : z1));
+                  for (int k = 0; k < 32; k += 2) {      // (the series' bits where a score is small)
+                    const float2 y = kv8_cap(mul2(pair(s[k], s[k + 1]), both(k < 16 ? z0 : z1)), cap2);
+                    s[k] = y.x;
+                    s[k + 1] = y.y;
+                  }
                 }
               } else {
                 const float z0 = sc[2 * c] * rowc, z1 = sc[2 * c + 1] * rowc;

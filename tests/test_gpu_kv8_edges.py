@@ -104,3 +104,33 @@ def test_nan_under_a_cap_stays_nan(T, dtype, cap):
     assert out[0, 2:, T - 1].isnan().all() and lse[0, 2:, T - 1].isnan().all()
     assert not out[0, :2].isnan().any() and not out[0, :, :T - 1].isnan().any()
     assert K.get_status() == 0
+
+
+@pytest.mark.parametrize("T,d", [(1, 128), (3, 64), (40, 128), (100, 64)])
+def test_capped_bits_do_not_depend_on_others(T, d):
+    """Under a cap, stale codes behind the length and a neighbouring row's large scores leave a row's bits
+    as they are."""
+    lay, data, qt, pos, _ = setup(300 + T, T, d, "f16", n=300)
+    lens = dev(np.array([299], np.int32))                 # 299 .. 303 stand in the last block
+    pos = dev(np.minimum(pos, 298))
+    (kcodes, kscales), v = data
+    vc = side(*v)
+    run = lambda q, codes: attend(q, pos, lens, side(codes, kscales), vc, 2, lay.cap, scoring=K.Scoring(softcap=64.0))
+    clean = kcodes.copy()
+    big = np.where(qt[0, 1, 0].numpy() > 0, 0x7e, 0xfe).astype(np.uint8)      # far above half the cap
+    for h in range(2):
+        clean[lay.rec(0, h, lay.cap)[299:]] = 0
+    dirty = clean.copy()
+    for h in range(2):
+        dirty[lay.rec(0, h, lay.cap)[299:]] = big
+    q = qt.cuda()
+    want = run(q, clean)
+    got = run(q, dirty)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    loud = q.clone()
+    loud[0, 1, 0] *= 64
+    got = run(loud, clean)
+    keep = torch.ones(want[1].shape, dtype=torch.bool, device="cuda")
+    keep[0, 1, 0] = False
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep], want[1][keep])
+    assert K.get_status() == 0
