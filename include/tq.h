@@ -604,7 +604,8 @@ tq_status tq_pages_reserve(const tq_page_pool* pool, const int32_t* rows, const 
  * DEVICE.  Makes row dst[i] continue from the first lens[i] tokens of row src[i]: whole pages
  * are shared (count + 1); a partly filled last page is copied, in every array, to a free page,
  * so that both rows can append.  dst rows are distinct, hold no pages and are none of src; one
- * src may be named many times.  All or nothing, with *shortfall as tq_pages_reserve.
+ * src may be named many times.  All or nothing, with *shortfall as tq_pages_reserve; it is -1 too
+ * where an entry among the first ceil(lens[i] / page_size) of row src[i] names no page in use.
  */
 tq_status tq_pages_fork(const tq_page_pool* pool, const tq_pool_array* arrays, int32_t n_arrays, const int32_t* src,
                         const int32_t* dst, const int32_t* lens, int32_t n, int32_t* shortfall, void* workspace,

@@ -313,7 +313,7 @@ tq_status run_attn(const AttnCall& c) {
 
 // ---- page pool
 struct PagesPlan {
-  size_t off_prefix, off_marks, off_from, off_to, bytes;
+  size_t off_prefix, off_marks, off_bad, off_from, off_to, bytes;
   int chunks;
 };
 
@@ -323,7 +323,8 @@ PagesPlan plan_pages(const tq_page_pool* pool, int64_t n) {
   const size_t pairs = static_cast<size_t>(std::max<int64_t>(n, pool->num_pages / 2 + 1)) * 4;
   P.off_prefix = up16(static_cast<size_t>(P.chunks) * 4);
   P.off_marks = P.off_prefix + up16(static_cast<size_t>(n + 1) * 4);
-  P.off_from = P.off_marks + up16(static_cast<size_t>((pool->rows + 31) / 32) * 8);
+  P.off_bad = P.off_marks + up16(static_cast<size_t>((pool->rows + 31) / 32) * 8);
+  P.off_from = P.off_bad + up16(static_cast<size_t>(kCheckBlocks) * 4);
   P.off_to = P.off_from + up16(pairs);
   P.bytes = P.off_to + up16(pairs);
   return P;
@@ -376,6 +377,7 @@ tq_status pool_scratch(const tq_page_pool* pool, int64_t n, void* ws, size_t ws_
   p.chunk_free = reinterpret_cast<int32_t*>(w);
   p.prefix = reinterpret_cast<int32_t*>(w + P.off_prefix);
   p.marks = reinterpret_cast<uint32_t*>(w + P.off_marks);
+  p.bad = reinterpret_cast<int32_t*>(w + P.off_bad);
   p.from = reinterpret_cast<int32_t*>(w + P.off_from);
   p.to = reinterpret_cast<int32_t*>(w + P.off_to);
   range = {ws, P.bytes};

@@ -27,6 +27,8 @@ constexpr int kThreads = 256;
 constexpr int kPer = kPageChunk / kThreads;  // counts a thread
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallPages = kSmallThreads * kPer, kSmallRequests = 2048, kSmallRows = 16384;
+constexpr int kSmallEntries = 32768;         // source entries of a fork that one block looks through
+static_assert(kCheckBlocks <= kThreads, "a thread reads one verdict");
 
 // Sum over the block; every thread gets it.
 template <int N = kThreads>
@@ -139,6 +141,8 @@ __device__ void scan_requests(const PagesParams& p, int* sh) {
 
 enum : int { COUNT_FORK = 0, COUNT_RESERVE = 1, COUNT_COMPACT = 2 };
 
+// Blocks: the chunks, one for the requests, and for a fork those that look through the source rows.
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p) {
   __shared__ int sh[kThreads / 32];
@@ -146,6 +150,24 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p) {
   pdl_trigger();
   if (MODE != COUNT_COMPACT && static_cast<int>(blockIdx.x) == p.chunks) {
     scan_requests<MODE == COUNT_FORK>(p, sh);
+    return;
+  }
+  if (MODE == COUNT_FORK && static_cast<int>(blockIdx.x) > p.chunks) {
+    const int first = blockIdx.x - p.chunks - 1;
+    bool ok = true;
+    for (int i = first; i < p.n; i += kCheckBlocks) {
+      int row, src, want;
+      if (!request<true>(p, i, row, src, want)) continue;        // (refused by the block of the requests)
+      const int used = pages_of(p.lens[i], p.pool.page_size);
+      const int32_t* from = p.pool.block_table + static_cast<int64_t>(src) * p.pool.max_pages;
+#pragma unroll 4
+      for (int c = threadIdx.x; c < used; c += kThreads) {
+        const int id = from[c];
+        ok &= id >= 0 && id < p.pool.num_pages && p.pool.refs[id] > 0;
+      }
+    }
+    const int bad = __syncthreads_or(!ok);
+    if (threadIdx.x == 0) p.bad[first] = bad;
     return;
   }
   int r[kPer];
@@ -175,8 +197,7 @@ __device__ __forceinline__ void share_pages(const PagesParams& p, int i) {
   for (int c = threadIdx.x; c < full; c += kThreads) {
     const int id = from[c];
     to[c] = id;
-    if (id >= 0 && id < pool.num_pages) atomicAdd(pool.refs + id, 1);
-    else report_status(p.status, TQ_ERR_INVALID_ARG);
+    atomicAdd(pool.refs + id, 1);
   }
 }
 
@@ -184,11 +205,7 @@ __device__ __forceinline__ void share_pages(const PagesParams& p, int i) {
 __device__ __forceinline__ int tail_page(const PagesParams& p, int i) {
   const tq_page_pool& pool = p.pool;
   const int len = p.lens[i];
-  if (len % pool.page_size == 0) return -1;
-  const int id = pool.block_table[static_cast<int64_t>(p.src[i]) * pool.max_pages + len / pool.page_size];
-  if (id >= 0 && id < pool.num_pages) return id;
-  report_status(p.status, TQ_ERR_INVALID_ARG);
-  return -1;
+  return len % pool.page_size ? pool.block_table[static_cast<int64_t>(p.src[i]) * pool.max_pages + len / pool.page_size] : -1;
 }
 
 // Gives page `id`, of rank `rank` among the free ones, to the request that wants it.
@@ -209,11 +226,15 @@ __device__ __forceinline__ void hand_out(const PagesParams& p, const int* prefix
 // Small pools: counts, requests and pages in one block.  A fork leaves prefix[n] = -1 where it changes
 // nothing.
 template <bool FORK>
-__global__ void __launch_bounds__(kSmallThreads) small_assign_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kSmallThreads, 1) small_assign_kernel(const PagesParams p) {
   __shared__ int sh[kSmallThreads / 32], prefix[kSmallRequests];
   __shared__ uint32_t marks[2][kSmallRows / 32];
   __shared__ uint16_t free_ids[kSmallPages];
+  __shared__ uint16_t in_use[kSmallThreads];   // bit k of word t: page t * kPer + k
   __shared__ int bad;
+  // (before free_ids is filled) a fork's source rows, and how many of their pages it asks for
+  uint16_t* srcs = free_ids;
+  uint16_t* used = free_ids + kSmallRequests;
   const int tid = threadIdx.x, words = (p.pool.rows + 31) / 32;
   for (int i = tid; i < words; i += kSmallThreads) marks[0][i] = marks[1][i] = 0;
   if (tid == 0) bad = 0;
@@ -222,6 +243,12 @@ __global__ void __launch_bounds__(kSmallThreads) small_assign_kernel(const Pages
   int r[kPer];
   const int64_t p0 = tid * kPer;
   load_refs(p.pool, p0, r);
+  if (FORK) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) bits |= (r[k] > 0 ? 1u : 0u) << k;
+    in_use[tid] = static_cast<uint16_t>(bits);
+  }
   __syncthreads();
   int need = 0;
   for (int i0 = 0; i0 < p.n; i0 += kSmallThreads) {
@@ -230,7 +257,11 @@ __global__ void __launch_bounds__(kSmallThreads) small_assign_kernel(const Pages
     if (i < p.n) {
       const bool ok = request<FORK>(p, i, row, src, want);
       if (!ok) want = 0;
-      if (FORK && ok) mark(marks[1], src);
+      if (FORK) {
+        if (ok) mark(marks[1], src);
+        srcs[i] = static_cast<uint16_t>(src);
+        used[i] = static_cast<uint16_t>(ok ? pages_of(p.lens[i], p.pool.page_size) : 0);
+      }
       if (!ok || mark(marks[0], row)) bad = 1;
     }
     const int before = block_before(want, sh);
@@ -241,6 +272,29 @@ __global__ void __launch_bounds__(kSmallThreads) small_assign_kernel(const Pages
   if (FORK)                                  // a row that is made must not be copied from too
     for (int i = tid; i < words; i += kSmallThreads)
       if (marks[0][i] & marks[1][i]) bad = 1;
+  if (FORK) {                                // every source row holds what it is asked for
+    // A warp takes two requests at a time, four steps of 32 entries of each, whose loads are in flight together.
+    constexpr int kWarps = kSmallThreads / 32;
+    bool ok = true;
+    for (int i = tid / 32; i < p.n; i += 2 * kWarps) {
+      const int i2 = min(i + kWarps, p.n - 1), n0 = used[i], n1 = used[i2];
+      const int32_t* from0 = p.pool.block_table + static_cast<int64_t>(srcs[i]) * p.pool.max_pages;
+      const int32_t* from1 = p.pool.block_table + static_cast<int64_t>(srcs[i2]) * p.pool.max_pages;
+      for (int c = tid % 32; c < max(n0, n1); c += 128) {
+        int id[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          id[k] = c + 32 * k < n0 ? from0[c + 32 * k] : 0;
+          id[4 + k] = c + 32 * k < n1 ? from1[c + 32 * k] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + 32 * (k & 3) < (k < 4 ? n0 : n1))
+            ok &= id[k] >= 0 && id[k] < p.pool.num_pages && (in_use[id[k] / kPer] >> id[k] % kPer & 1);
+      }
+    }
+    if (!ok) bad = 1;
+  }
   const int mine = count_free(r);
   int rank = block_before(mine, sh);
   const int all = block_sum<kSmallThreads>(mine, sh);
@@ -274,7 +328,8 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
   pdl_wait();
   pdl_trigger();
   const tq_page_pool& pool = p.pool;
-  const int need = p.prefix[p.n];
+  int need = p.prefix[p.n];
+  if (FORK && __syncthreads_or(static_cast<int>(threadIdx.x) < min(p.n, kCheckBlocks) && p.bad[threadIdx.x])) need = -1;
   int before, all;
   chunk_sums(p, blockIdx.x, sh, before, all);
   const bool short_of = need < 0 || all < need;
@@ -482,7 +537,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const PagesParams p) {
     int from, to;
     if (MODE == COPY_LIST) { from = p.src[j]; to = p.rows[j]; }
     else { to = p.to[j]; from = MODE == COPY_FORK && to < 0 ? -1 : p.from[j]; }
-    if (MODE == COPY_FORK && (to < 0 || from < 0)) continue;
+    if (MODE == COPY_FORK && to < 0) continue;
     if (from < 0 || from >= n_pages || to < 0 || to >= n_pages) {
       if (threadIdx.x == 0) report_status(p.status, TQ_ERR_INVALID_ARG);
       continue;
@@ -514,7 +569,8 @@ cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t s) {
 
 // One block does it (small_assign_kernel).
 static bool is_small(const PagesParams& p) {
-  return p.pool.num_pages <= kSmallPages && p.n <= kSmallRequests && p.pool.rows <= kSmallRows;
+  return p.pool.num_pages <= kSmallPages && p.n <= kSmallRequests && p.pool.rows <= kSmallRows &&
+         (!p.src || static_cast<int64_t>(p.n) * p.pool.max_pages <= kSmallEntries);
 }
 
 cudaError_t launch_pages_reserve(const PagesParams& p, cudaStream_t s) {
@@ -529,7 +585,7 @@ cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t s) {
     const unsigned grid = std::max(copy_grid(p.n, p, sms), std::min(static_cast<unsigned>(p.n), 8u * sms));
     return e != cudaSuccess ? e : launch_pdl(copy_kernel<COPY_SMALL_FORK>, dim3(grid), dim3(kThreads), 0, s, p);
   }
-  cudaError_t e = launch_pdl(count_kernel<COUNT_FORK>, dim3(p.chunks + 1), dim3(kThreads), 0, s, p);
+  cudaError_t e = launch_pdl(count_kernel<COUNT_FORK>, dim3(p.chunks + 1 + std::min(p.n, kCheckBlocks)), dim3(kThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(assign_kernel<true>, dim3(p.chunks + p.n), dim3(kThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(copy_kernel<COPY_FORK>, dim3(copy_grid(p.n, p, sms)), dim3(kThreads), 0, s, p);
   return e;

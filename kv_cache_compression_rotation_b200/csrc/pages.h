@@ -11,6 +11,7 @@ namespace tq {
 
 constexpr int kPageChunk = 4096;             // reference counts a block
 constexpr int kCopySlice = 16384;            // bytes of a page that a block moves at a time
+constexpr int kCheckBlocks = 256;            // blocks that look through the source rows of a fork
 
 struct PoolCopy {                            // the arrays whose pages move together
   char* data[TQ_MAX_POOL_ARRAYS];
@@ -34,6 +35,7 @@ struct PagesParams {
   int32_t* chunk_free;                       // [chunks] free pages of each chunk
   int32_t* prefix;                           // [n + 1] pages wanted before each request; [n] = -1: refused
   uint32_t* marks;                           // [2][(rows + 31) / 32]
+  int32_t* bad;                              // [kCheckBlocks] fork: a source row lacks pages
   int32_t* from;                             // page copies: pairs
   int32_t* to;
   int chunks;

@@ -1,5 +1,5 @@
-"""GPU tests of the page pool's calls at their edges: pools without arrays, in the form of one block and
-the form of many, against the oracle (whole numbers, all equal)."""
+"""GPU tests of the page pool's calls at their edges, in the form of one block and the form of many: pools
+without arrays against the oracle (whole numbers, all equal), source rows that lack pages."""
 import numpy as np
 import pytest
 
@@ -61,3 +61,34 @@ def test_pool_without_arrays(rows, mp, page, pages):
         assert np.array_equal(got.cpu().numpy(), page_map) and live.item() == n
         check()
     assert K.get_status() == 0
+
+
+@pytest.mark.parametrize("rows,mp,pages", [(6, 8, 40), (6, 8, 17000), (300, 400, 6000)],
+                         ids=["one_block", "many_pages", "many_entries"])
+def test_fork_of_a_row_that_lacks_pages_changes_nothing(rows, mp, pages):
+    """Entries that were never given, that name a free page or none of the pool, in the whole pages or
+    in the tail: the call is refused whole, whatever its other requests are."""
+    page, n = 16, 5 * 16 + 7
+    table = torch.full((rows, mp), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    data = torch.arange(pages * 4, dtype=torch.int32, device="cuda")
+    pool = K.PagePool(table, refs, page, [data])
+    assert K.pages_reserve(pool, i32([0, 1]), i32([0, 0]), i32([n, n])).item() == 0
+    good = table.clone()
+    many = rows - 2 if rows > 100 else 4
+    dst = list(range(2, 2 + many))
+    for col, entry, length in ((5, -1, n), (2, -1, n), (0, pages - 1, n), (5, pages, n), (3, 1 << 30, n), (0, -5, 1), (6, -1, 16 * 7),
+                               (6, -1, 16 * 6 + 1)):
+        for where in (0, many - 1):
+            table.copy_(good)
+            if col < 6:
+                table[1, col] = entry
+            state = [t.clone() for t in (table, refs, data)]
+            src, lens = [0] * many, [n] * many
+            src[where], lens[where] = 1, length
+            assert K.pages_fork(pool, i32(src), i32(dst), i32(lens)).item() == -1 and K.get_status() == 1
+            for t, x in zip((table, refs, data), state):
+                assert torch.equal(t, x)
+    table.copy_(good)
+    assert K.pages_fork(pool, i32([0, 1]), i32([2, 3]), i32([n, n])).item() == 0 and K.get_status() == 0
+    assert torch.equal(table[2:4, :5], table[:2, :5]) and refs.sum().item() == 12 + 10 + 2
