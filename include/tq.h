@@ -592,9 +592,9 @@ tq_status tq_pages_free(const tq_page_pool* pool, const int32_t* rows, const int
 /*
  * DEVICE.  Grows rows[i] from old_lens[i] to new_lens[i] tokens: the entries between the two
  * page counts get free pages (count 1).  Rows are distinct.  All or nothing: *shortfall (device
- * int32) is 0 when done; else nothing changed and it holds the number of pages lacking, or -1
- * for a repeated row or one out of range, or a length out of range (device status
- * TQ_ERR_INVALID_ARG).
+ * int32) is 0 when done; else nothing changed and it holds the number of pages lacking (of at
+ * most 2^31 - 1 that are wanted), or -1 for a repeated row or one out of range, or a length out of
+ * range (device status TQ_ERR_INVALID_ARG).
  */
 tq_status tq_pages_reserve(const tq_page_pool* pool, const int32_t* rows, const int32_t* old_lens,
                            const int32_t* new_lens, int32_t n, int32_t* shortfall, void* workspace, size_t ws_bytes,

@@ -34,36 +34,41 @@ constexpr int kSmallEntries = 65535;
 static_assert(kCheckBlocks <= kThreads, "a thread reads one verdict");
 
 // Sum over the block; every thread gets it.
-template <int N = kThreads>
-__device__ __forceinline__ int block_sum(int x, int* sh) {
+template <int N = kThreads, typename T>
+__device__ __forceinline__ T block_sum(T x, T* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   __syncthreads();
   if (lane == 0) sh[warp] = x;
   __syncthreads();
-  int t = 0;
+  T t = 0;
 #pragma unroll
   for (int w = 0; w < N / 32; ++w) t += sh[w];
   return t;
 }
 
 // Sum over the threads before this one.
-__device__ __forceinline__ int block_before(int x, int* sh) {
+template <typename T>
+__device__ __forceinline__ T block_before(T x, T* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = x;
+  T s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = s;
   __syncthreads();
-  int t = s - x;
+  T t = s - x;
   for (int w = 0; w < warp; ++w) t += sh[w];
   return t;
 }
+
+// Pages that requests want (their sum may pass 32 bits); no pool has as many as INT32_MAX.
+using Wanted = long long;
+__device__ __forceinline__ int pages_wanted(Wanted n) { return static_cast<int>(min(n, static_cast<Wanted>(INT32_MAX))); }
 
 __device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
 
@@ -113,13 +118,14 @@ __device__ __forceinline__ bool request(const PagesParams& p, int i, int& row, i
 
 // The last block: what the requests want, and whether they can be served at all.
 template <bool FORK>
-__device__ void scan_requests(const PagesParams& p, int* sh) {
+__device__ void scan_requests(const PagesParams& p) {
+  __shared__ Wanted sh[kThreads / 32];
   __shared__ int bad;
   const int words = (p.pool.rows + 31) / 32;
   if (threadIdx.x == 0) bad = 0;
   for (int i = threadIdx.x; i < 2 * words; i += kThreads) p.marks[i] = 0;
   __syncthreads();
-  int run = 0;
+  Wanted run = 0;
   for (int i0 = 0; i0 < p.n; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     int want = 0;
@@ -130,16 +136,16 @@ __device__ void scan_requests(const PagesParams& p, int* sh) {
       if (FORK && ok) mark(p.marks + words, src);
       if (!ok || mark(p.marks, row)) atomicOr(&bad, 1);
     }
-    const int before = block_before(want, sh);
-    if (i < p.n) p.prefix[i] = run + before;
-    run += block_sum(want, sh);
+    const Wanted before = block_before(static_cast<Wanted>(want), sh);
+    if (i < p.n) p.prefix[i] = pages_wanted(run + before);
+    run += block_sum(static_cast<Wanted>(want), sh);
   }
   __syncthreads();
   if (FORK)                                  // a row that is made must not be copied from too
     for (int i = threadIdx.x; i < words; i += kThreads)
       if (p.marks[i] & p.marks[words + i]) atomicOr(&bad, 1);
   __syncthreads();
-  if (threadIdx.x == 0) p.prefix[p.n] = bad ? -1 : run;
+  if (threadIdx.x == 0) p.prefix[p.n] = bad ? -1 : pages_wanted(run);
 }
 
 enum : int { COUNT_FORK = 0, COUNT_RESERVE = 1, COUNT_COMPACT = 2 };
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p) {
   pdl_wait();
   pdl_trigger();
   if (MODE != COUNT_COMPACT && static_cast<int>(blockIdx.x) == p.chunks) {
-    scan_requests<MODE == COUNT_FORK>(p, sh);
+    scan_requests<MODE == COUNT_FORK>(p);
     return;
   }
   if (MODE == COUNT_FORK && static_cast<int>(blockIdx.x) > p.chunks) {
@@ -230,6 +236,7 @@ __device__ __forceinline__ void hand_out(const PagesParams& p, const int* prefix
 // nothing.
 template <bool FORK>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_assign_kernel(const PagesParams p) {
+  __shared__ Wanted sh_wanted[kSmallThreads / 32];
   __shared__ int sh[kSmallThreads / 32], prefix[kSmallRequests];
   __shared__ uint32_t marks[2][kSmallRows / 32];
   __shared__ uint16_t free_ids[kSmallPages];
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_assign_kernel(const Pa
     in_use[tid] = static_cast<uint16_t>(bits);
   }
   __syncthreads();
-  int need = 0;
+  Wanted sum = 0;
   for (int i0 = 0; i0 < p.n; i0 += kSmallThreads) {
     const int i = i0 + tid;
     int row = 0, src = 0, want = 0;
@@ -267,10 +274,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_assign_kernel(const Pa
       }
       if (!ok || mark(marks[0], row)) bad = 1;
     }
-    const int before = block_before(want, sh);
-    if (i < p.n) prefix[i] = need + before;
-    need += block_sum<kSmallThreads>(want, sh);
+    const Wanted before = block_before(static_cast<Wanted>(want), sh_wanted);
+    if (i < p.n) prefix[i] = pages_wanted(sum + before);
+    sum += block_sum<kSmallThreads>(static_cast<Wanted>(want), sh_wanted);
   }
+  const int need = pages_wanted(sum);
   __syncthreads();
   if (FORK)                                  // a row that is made must not be copied from too
     for (int i = tid; i < words; i += kSmallThreads)

@@ -92,3 +92,19 @@ def test_fork_of_a_row_that_lacks_pages_changes_nothing(rows, mp, pages):
     table.copy_(good)
     assert K.pages_fork(pool, i32([0, 1]), i32([2, 3]), i32([n, n])).item() == 0 and K.get_status() == 0
     assert torch.equal(table[2:4, :5], table[:2, :5]) and refs.sum().item() == 12 + 10 + 2
+
+
+@pytest.mark.parametrize("pages", [64, 20000])
+@pytest.mark.parametrize("rows", [2, 3, 4, 5])
+def test_more_pages_wanted_than_32_bits_count(rows, pages):
+    """rows x 2^30 pages are wanted (a table of up to 21 GB, of which nothing is touched): refused for want of
+    pages, whatever the sum is modulo 2^32."""
+    mp = 1 << 30
+    table = torch.empty((rows, mp), dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[7] = 1
+    pool = K.PagePool(table, refs, 1)
+    edge = table[:, :8].clone()
+    short = K.pages_reserve(pool, i32(range(rows)), i32([0] * rows), i32([mp] * rows)).item()
+    assert short == 2 ** 31 - 1 - (pages - 1) and K.get_status() == 0
+    assert refs.sum().item() == 1 and torch.equal(table[:, :8], edge)
