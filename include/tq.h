@@ -528,8 +528,9 @@ tq_status tq_kv8_attn_workspace(int32_t dtype, int32_t B, int32_t Hq, int32_t Hk
  * position kv_lens[b] - 1 and, with KV head h / (Hq/Hkv),
  *   out = sum_t softmax_t(s) v^_t,   lse = ln sum_t e^s   (scores as tq_scoring).
  * q [B][Hq][d] (dtype; q_strides.t unused), out [B][Hq][d] of the same dtype, lse [B][Hq] fp32
- * or NULL.  kv_lens[b] may be 0.  With k_new / v_new [B][Hkv][d] (both or neither; strides .b
- * and .h) the step's token kv_lens[b] - 1 is appended first, as tq_kv8_append with T = 1.
+ * or NULL.  kv_lens[b] may be 0 (a place of the batch that is not in use).  With k_new / v_new
+ * [B][Hkv][d] (both or neither; strides .b and .h) the step's token kv_lens[b] - 1 is appended first,
+ * as tq_kv8_append with T = 1; a sequence with kv_lens[b] = 0 brings none.
  * pages NULL: the [B][Hkv][Nmax] layout; else Nmax is ignored.  A length outside 0..capacity
  * is read as the nearest bound and reported; NaN codes of value records that some query of the
  * step does not see are read as 0, so they never reach it.

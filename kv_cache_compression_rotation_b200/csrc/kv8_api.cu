@@ -255,6 +255,7 @@ tq_status run_attn(const AttnCall& c) {
     Range fresh[2];
     if ((s = prepare_append(*c.append, c.dtype, c.B, c.Hkv, c.d, c.kv_lens, m, recs, c.pages, c.kc, c.vc, ap, fresh)) != TQ_OK)
       return s;
+    ap.empty_ok = true;
     Range caches[4];
     kv8_ranges(c.kc, recs, c.d, caches);
     kv8_ranges(c.vc, recs, c.d, caches + 2);

@@ -29,6 +29,7 @@ struct Kv8AppendParams {
   int dtype, B, T, blocks;                            // blocks: that T new tokens can touch
   const int32_t* kv_lens;
   const int32_t* new_lens;                            // or nullptr: T
+  bool empty_ok;                                      // a sequence of no tokens brings none (decode steps)
   uint8_t* codes[2];
   float* scales[2];
   Kv8Map map;

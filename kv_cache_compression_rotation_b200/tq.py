@@ -784,7 +784,8 @@ def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 
                     k_new=None, v_new=None, scoring: Optional[Scoring] = None, out=None, lse=None,
                     return_lse: bool = False, workspace=None, stream=None):
     """tq_kv8_decode_attn: one step for q [B, Hq, d], output of q's dtype (with lse fp32 [B, Hq] when
-    return_lse); k_new / v_new [B, Hkv, d] are appended as token kv_lens[b] - 1 first."""
+    return_lse); k_new / v_new [B, Hkv, d] are appended as token kv_lens[b] - 1 first (none where
+    kv_lens[b] is 0)."""
     B, Hq, d = q.shape
     cap, scoring = _kv8_attn_checks(B, Hq, 1, d, kcache, vcache, Hkv, Nmax, pages, scoring)
     _same_device(q.device, kv_lens, kcache.codes, vcache.codes, k_new, v_new, out, lse, workspace, scoring.slopes,

@@ -134,3 +134,30 @@ def test_capped_bits_do_not_depend_on_others(T, d):
     keep[0, 1, 0] = False
     assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep], want[1][keep])
     assert K.get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_step_with_append_and_places_not_in_use(dtype):
+    """A padded batch: sequences of no tokens bring none, keep their pages as they are and get zeros; nothing
+    is reported, and the others get what a batch of their own gives them."""
+    r = H.rng(400)
+    B, Hq, Hkv, d = 5, 4, 2, 128
+    lay = H.Layout(r, B, Hkv, 64, 16)
+    data = [H.random_side(r, lay.records, d) for _ in range(2)]
+    lens = np.array([0, 33, 0, 1, 0], np.int32)
+    used = [1, 3]
+    q, kn, vn = (torch.from_numpy(r.standard_normal((B, h, d)).astype(np.float32)).to(DT[dtype]).cuda() for h in (Hq, Hkv, Hkv))
+    table = lay.table.copy()
+    table[lens == 0] = -1                                 # they need no pages
+    sides = [[side(c, s) for c, s in data] for _ in range(2)]
+    out, lse = K.kv8_decode_attn(q, dev(lens), *sides[0], Hkv, pages=K.Pages(dev(table), 16, lay.num_pages), k_new=kn, v_new=vn,
+                                 return_lse=True)
+    assert K.get_status() == 0
+    want = K.kv8_decode_attn(q[used], dev(lens[used]), *sides[1], Hkv, pages=K.Pages(dev(table[used]), 16, lay.num_pages),
+                             k_new=kn[used], v_new=vn[used], return_lse=True)
+    assert K.get_status() == 0
+    assert torch.equal(out[used], want[0]) and torch.equal(lse[used], want[1])
+    empty = [0, 2, 4]
+    assert not out[empty].any() and (lse[empty] == -math.inf).all()
+    for a, b in zip(*sides):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
