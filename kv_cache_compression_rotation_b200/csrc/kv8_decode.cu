@@ -198,6 +198,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   };
   auto ask = [&]() {
     Next n{0, 0, -1};
+    if (iu >= u1) return n;                  // (asked again behind the last tile)
     bool moved = false;
     while (ij >= ir.tiles) {
       ij -= ir.tiles;
