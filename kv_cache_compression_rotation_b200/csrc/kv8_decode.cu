@@ -150,12 +150,11 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   const uint32_t bar0 = base + L.bars + warp * NS * 8;
   const uint32_t sc0 = base + L.scales + warp * NS * NB * 8;
   const int ppb = static_cast<int>(p.map.page / kKv8Block);
-  if (lane == 0)
+  if (lane == 0) {                           // (each warp's own barriers; the fence is for the thread's own)
     for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1 + 2 * NB);
-  if (tid == 0) {
-    *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) *abort_flag = 0;
   if (!p.appended) pdl_wait();               // (behind an append nothing that it writes is read before the second wait)
 
   // ---- how the work is cut
