@@ -26,19 +26,6 @@ struct Kv8Map {
   int64_t cap;            // tokens a sequence can hold
 };
 
-// Record of token t; an id outside the pool is read as page 0 and reported.
-__device__ __forceinline__ int64_t kv8_record(const Kv8Map& m, int b, int h, int64_t t, int* status) {
-  if (!m.table) return (static_cast<int64_t>(b) * m.Hkv + h) * m.page + t;
-  const int page = static_cast<int>(m.page);
-  const int ti = static_cast<int>(t), col = ti / page;
-  int64_t id = __ldg(m.table + static_cast<int64_t>(b) * m.max_pages + col);
-  if (id < 0 || id >= m.num_pages) {
-    report_status(status, TQ_ERR_INVALID_ARG);
-    id = 0;
-  }
-  return (id * m.Hkv + h) * page + (ti - col * page);
-}
-
 // Which tokens a query at `pos` sees, and how its scores are formed.
 struct Kv8Scoring {
   const int32_t* kv_lens;   // [B]
