@@ -704,6 +704,13 @@ def _ints(t, n: int, name: str):
     return t.data_ptr()
 
 
+def _scratch(t):
+    """A caller's workspace: numel() stands for its bytes, which must be there one after the other."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t
+
+
 def _rows(t, name: str, d: int):
     if t.stride(-1) != 1 or t.shape[-1] != d:
         raise ValueError(f"{name}: the last dimension must be {d} contiguous elements")
@@ -816,7 +823,9 @@ def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, B, Hq, Hkv, 
         lse = kcache.scales.new_empty(shape[:-1]) if return_lse else None
     elif lse.shape != shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor {tuple(shape[:-1])}")
-    if workspace is None:
+    if workspace is not None:
+        _scratch(workspace)
+    else:
         workspace = torch.empty(kv8_workspace_bytes(q.dtype, B, Hq, Hkv, T, d, cap), dtype=torch.uint8, device=q.device)
     return out, lse, workspace
 
@@ -902,7 +911,7 @@ def pages_reserve(pool: PagePool, rows, old_lens, new_lens, shortfall=None, work
     n = rows.numel()
     _same_device(pool.device, rows, old_lens, new_lens, shortfall, workspace)
     shortfall = _one_int(pool) if shortfall is None else shortfall
-    ws = pool._work(n) if workspace is None else workspace
+    ws = pool._work(n) if workspace is None else _scratch(workspace)
     _check(lib().tq_pages_reserve(C.byref(pool.c), _ints(rows, n, "rows"), _ints(old_lens, n, "old_lens"),
                                   _ints(new_lens, n, "new_lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(),
                                   ws.numel(), _stream(stream)))
@@ -916,7 +925,7 @@ def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, s
     n = src.numel()
     _same_device(pool.device, src, dst, lens, shortfall, workspace)
     shortfall = _one_int(pool) if shortfall is None else shortfall
-    ws = pool._work(n) if workspace is None else workspace
+    ws = pool._work(n) if workspace is None else _scratch(workspace)
     _check(lib().tq_pages_fork(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(src, n, "src"), _ints(dst, n, "dst"),
                                _ints(lens, n, "lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(), ws.numel(),
                                _stream(stream)))
@@ -930,7 +939,7 @@ def pages_compact(pool: PagePool, page_map=None, live=None, workspace=None, stre
     _same_device(pool.device, page_map, live, workspace)
     page_map = pool.refs.new_empty(pool.num_pages) if page_map is None else page_map
     live = _one_int(pool) if live is None else live
-    ws = pool._work(0) if workspace is None else workspace
+    ws = pool._work(0) if workspace is None else _scratch(workspace)
     _check(lib().tq_pages_compact(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(page_map, pool.num_pages, "page_map"),
                                   _ints(live, 1, "live"), ws.data_ptr(), ws.numel(), _stream(stream)))
     return page_map

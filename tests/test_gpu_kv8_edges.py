@@ -161,3 +161,20 @@ def test_step_with_append_and_places_not_in_use(dtype):
     assert not out[empty].any() and (lse[empty] == -math.inf).all()
     for a, b in zip(*sides):
         assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+
+
+def test_workspaces_that_are_not_contiguous_are_refused():
+    """Nothing is launched for a workspace whose elements share memory."""
+    lay, data, qt, pos, lens = setup(500, 40, 64, "bf16")
+    kc, vc = (side(c, s) for c, s in data)
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 26)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    pool = K.PagePool(torch.full((4, 4), -1, dtype=torch.int32, device="cuda"), torch.zeros(16, dtype=torch.int32, device="cuda"), 16)
+    for call in (lambda: attend(qt.cuda(), dev(pos), lens, kc, vc, 2, lay.cap, workspace=one),
+                 lambda: attend(qt.cuda()[:, :, :1], None, lens, kc, vc, 2, lay.cap, workspace=one),
+                 lambda: K.pages_reserve(pool, i32(0), i32(0), i32(9), workspace=one),
+                 lambda: K.pages_fork(pool, i32(0), i32(1), i32(9), workspace=one),
+                 lambda: K.pages_compact(pool, workspace=one)):
+        with pytest.raises(ValueError):
+            call()
+    assert K.get_status() == 0
