@@ -215,25 +215,28 @@ def _tensors(x):
     return [x] if hasattr(x, "record_stream") else []
 
 
+def _allocated(stream, f, *args):
+    """f(*args), which allocates, with `stream` as the current one, so that the memory belongs to it: a
+    workspace that is dropped at return goes to nobody else while the kernels use it, and an output's
+    memory to nobody while the caller's stream reads it."""
+    import torch
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        result = f(*args)
+    if here != stream:
+        for t in _tensors(result):
+            t.record_stream(here)
+    return result
+
+
 def _on_stream(f):
-    """For calls that allocate.  With stream= they run as if it were the current stream, so that what
-    they allocate belongs to it: a workspace that is dropped at return goes to nobody else while the
-    kernels use it, and an output's memory to nobody while the caller's stream reads it."""
+    """For calls that allocate: with stream= the whole call runs as if that were the current stream."""
     at = list(inspect.signature(f).parameters).index("stream")
 
     @functools.wraps(f)
     def call(*args, **kw):
         stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None:
-            return f(*args, **kw)
-        import torch
-        here = torch.cuda.current_stream(stream.device)
-        with torch.cuda.stream(stream):
-            result = f(*args, **kw)
-        if here != stream:
-            for t in _tensors(result):
-                t.record_stream(here)
-        return result
+        return f(*args, **kw) if stream is None else _allocated(stream, functools.partial(f, **kw), *args)
 
     return call
 
@@ -786,7 +789,6 @@ def _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring):
     return cap, scoring
 
 
-@_on_stream
 def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0, pages: Optional[Pages] = None,
                     k_new=None, v_new=None, scoring: Optional[Scoring] = None, out=None, lse=None,
                     return_lse: bool = False, workspace=None, stream=None):
@@ -803,7 +805,7 @@ def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 
                 k_new.dtype is not q.dtype or v_new.dtype is not q.dtype:
             raise ValueError(f"k_new and v_new must be [{B}, {Hkv}, {d}] of q's dtype")
         kst, vst = (C.byref(Strides_t(t.stride(0), t.stride(1), 0)) for t in (k_new, v_new))
-    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, d), out, lse, return_lse, workspace, B, Hq, Hkv, 1, d, cap)
+    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, d), out, lse, return_lse, workspace, stream, B, Hq, Hkv, 1, d, cap)
     _check(lib().tq_kv8_decode_attn(_rows(q, "q", d), C.byref(Strides_t(q.stride(0), q.stride(1), 0)), _dtype_code(q), B,
                                     Hq, Hkv, d, _ints(kv_lens, B, "kv_lens"), C.byref(scoring.as_c(d)),
                                     None if pages is None else pages.ref, Nmax,
@@ -813,8 +815,10 @@ def kv8_decode_attn(q, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 
     return (out, lse) if return_lse else out
 
 
-def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap):
+def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, stream, *call):
     import torch
+    if stream is not None:
+        return _allocated(stream, _kv8_outputs, q, kcache, shape, out, lse, return_lse, workspace, None, *call)
     if out is None:                            # (new_empty costs the host a third less than empty)
         out = q.new_empty(shape)
     elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
@@ -826,11 +830,10 @@ def _kv8_outputs(q, kcache, shape, out, lse, return_lse, workspace, B, Hq, Hkv, 
     if workspace is not None:
         _scratch(workspace)
     else:
-        workspace = torch.empty(kv8_workspace_bytes(q.dtype, B, Hq, Hkv, T, d, cap), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(kv8_workspace_bytes(q.dtype, *call), dtype=torch.uint8, device=q.device)
     return out, lse, workspace
 
 
-@_on_stream
 def kv8_prefill_attn(q, q_pos, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax: int = 0,
                      pages: Optional[Pages] = None, scoring: Optional[Scoring] = None, out=None, lse=None,
                      return_lse: bool = False, workspace=None, stream=None):
@@ -840,7 +843,7 @@ def kv8_prefill_attn(q, q_pos, kv_lens, kcache: Kv8, vcache: Kv8, Hkv: int, Nmax
     cap, scoring = _kv8_attn_checks(B, Hq, T, d, kcache, vcache, Hkv, Nmax, pages, scoring)
     _same_device(q.device, q_pos, kv_lens, kcache.codes, vcache.codes, out, lse, workspace, scoring.slopes,
                  scoring.first, scoring.prefix)
-    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, T, d), out, lse, return_lse, workspace, B, Hq, Hkv, T, d, cap)
+    out, lse, ws = _kv8_outputs(q, kcache, (B, Hq, T, d), out, lse, return_lse, workspace, stream, B, Hq, Hkv, T, d, cap)
     st = q.stride()
     _check(lib().tq_kv8_prefill_attn(_rows(q, "q", d), C.byref(Strides_t(st[0], st[1], st[2])), _dtype_code(q), B, Hq, Hkv,
                                      T, d, _ints(q_pos, B * T, "q_pos"), _ints(kv_lens, B, "kv_lens"),
@@ -893,8 +896,11 @@ class PagePool:
         return torch.empty(size, dtype=torch.uint8, device=self.device)
 
 
-def _one_int(pool: PagePool):
-    return pool.refs.new_empty(1)
+def _pool_outputs(pool: PagePool, n: int, out, size: int, workspace, stream):
+    """An int32 output of `size` values and the workspace of n requests, where they are not given."""
+    if stream is not None:
+        return _allocated(stream, _pool_outputs, pool, n, out, size, workspace, None)
+    return (pool.refs.new_empty(size) if out is None else out), (pool._work(n) if workspace is None else _scratch(workspace))
 
 
 def pages_free(pool: PagePool, rows, lens, stream=None) -> None:
@@ -904,42 +910,37 @@ def pages_free(pool: PagePool, rows, lens, stream=None) -> None:
     _check(lib().tq_pages_free(C.byref(pool.c), _ints(rows, n, "rows"), _ints(lens, n, "lens"), n, _stream(stream)))
 
 
-@_on_stream
 def pages_reserve(pool: PagePool, rows, old_lens, new_lens, shortfall=None, workspace=None, stream=None):
     """tq_pages_reserve: rows int32 [n] grow from old_lens to new_lens tokens.  Returns the device
     int32 [1] shortfall (0 = done)."""
     n = rows.numel()
     _same_device(pool.device, rows, old_lens, new_lens, shortfall, workspace)
-    shortfall = _one_int(pool) if shortfall is None else shortfall
-    ws = pool._work(n) if workspace is None else _scratch(workspace)
+    shortfall, ws = _pool_outputs(pool, n, shortfall, 1, workspace, stream)
     _check(lib().tq_pages_reserve(C.byref(pool.c), _ints(rows, n, "rows"), _ints(old_lens, n, "old_lens"),
                                   _ints(new_lens, n, "new_lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(),
                                   ws.numel(), _stream(stream)))
     return shortfall
 
 
-@_on_stream
 def pages_fork(pool: PagePool, src, dst, lens, shortfall=None, workspace=None, stream=None):
     """tq_pages_fork: row dst[i] continues from the first lens[i] tokens of row src[i] (int32 [n]
     each).  Returns the device int32 [1] shortfall (0 = done)."""
     n = src.numel()
     _same_device(pool.device, src, dst, lens, shortfall, workspace)
-    shortfall = _one_int(pool) if shortfall is None else shortfall
-    ws = pool._work(n) if workspace is None else _scratch(workspace)
+    shortfall, ws = _pool_outputs(pool, n, shortfall, 1, workspace, stream)
     _check(lib().tq_pages_fork(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(src, n, "src"), _ints(dst, n, "dst"),
                                _ints(lens, n, "lens"), n, _ints(shortfall, 1, "shortfall"), ws.data_ptr(), ws.numel(),
                                _stream(stream)))
     return shortfall
 
 
-@_on_stream
 def pages_compact(pool: PagePool, page_map=None, live=None, workspace=None, stream=None):
     """tq_pages_compact: live pages move to the lowest ids.  Returns page_map int32 [num_pages] (new
     id of each page, -1: free); live int32 [1], where given, receives their number."""
     _same_device(pool.device, page_map, live, workspace)
-    page_map = pool.refs.new_empty(pool.num_pages) if page_map is None else page_map
-    live = _one_int(pool) if live is None else live
-    ws = pool._work(0) if workspace is None else _scratch(workspace)
+    page_map, ws = _pool_outputs(pool, 0, page_map, pool.num_pages, workspace, stream)
+    if live is None:
+        live = pool.refs.new_empty(1) if stream is None else _allocated(stream, pool.refs.new_empty, 1)
     _check(lib().tq_pages_compact(C.byref(pool.c), pool.pa, len(pool.arrays), _ints(page_map, pool.num_pages, "page_map"),
                                   _ints(live, 1, "live"), ws.data_ptr(), ws.numel(), _stream(stream)))
     return page_map
