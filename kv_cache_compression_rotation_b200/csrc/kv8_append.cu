@@ -94,8 +94,7 @@ kv8_append_kernel(const Kv8AppendParams p) {
   if (side > 1) return;
 
   const int len = __ldg(p.kv_lens + b);
-  if (p.empty_ok && len == 0) return;
-  const int fresh = p.new_lens ? __ldg(p.new_lens + b) : p.T;
+  const int fresh = p.new_lens ? __ldg(p.new_lens + b) : p.empty_ok && len == 0 ? 0 : p.T;
   if (fresh < 0 || fresh > p.T || len < fresh || len > p.map.cap) {
     report_status(p.status, TQ_ERR_INVALID_ARG);
     return;

@@ -439,13 +439,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
               s[bl][nt][k] = y.x;
               s[bl][nt][k + 1] = y.y;
             }
-      } else {
-#pragma unroll
-        for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[bl][nt][k] *= ksc[bl] * cs[nt][k & 1];
       }
       float mx[NT][2];
 #pragma unroll
@@ -457,7 +450,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int c = k & 1, t = t0 + bl * 16 + g + (k >> 1) * 8;
-            float x = s[bl][nt][k];
+            float x = s[bl][nt][k] * (p.sc.cap > 0.f ? 1.f : ksc[bl] * cs[nt][c]);
             if (p.sc.slopes) x -= slope[nt][c] * static_cast<float>(abs(pos[nt][c] - t));
             if (masked && (t < lo[nt][c] || t >= hi[nt][c])) x = -INFINITY;
             s[bl][nt][k] = x;

@@ -178,3 +178,28 @@ def test_workspaces_that_are_not_contiguous_are_refused():
         with pytest.raises(ValueError):
             call()
     assert K.get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_infinities_and_nans_that_are_appended(dtype):
+    """An infinity takes the largest code (its block's scale is 2^120, so finite neighbours become 0), a NaN
+    the NaN code and no part in the scale; other blocks are as without them."""
+    r = H.rng(600)
+    x = r.standard_normal((1, 1, 48, 64)).astype(np.float32)
+    x[0, 0, 3, 5], x[0, 0, 9, 60], x[0, 0, 20, 7] = np.inf, -np.inf, np.nan
+    t = torch.from_numpy(x).to(DT[dtype])
+    kc, vc = (K.kv8_alloc(48, 64) for _ in range(2))
+    K.kv8_append(kc, vc, t.cuda(), t.cuda(), dev(np.array([48], np.int32)), Nmax=48)
+    assert K.get_status() == 0
+    want, scales = np.zeros((48, 64), np.uint8), np.zeros(3, np.float32)
+    O.append(want, scales, np.arange(48), np.nan_to_num(t.double().numpy()[0, 0], nan=0.0, posinf=0.0, neginf=0.0), 0)
+    for c in (kc, vc):
+        codes, sc = c.codes.cpu().numpy(), c.scales.cpu().numpy()
+        assert sc[0] == 2.0 ** 120 and np.array_equal(sc[1:], scales[1:])
+        assert codes[3, 5] == 0x7e and codes[9, 60] == 0xfe and (codes[20, 7] & 0x7f) == 0x7f
+        rest = codes[:16].copy()
+        rest[3, 5] = rest[9, 60] = 0
+        assert not (rest & 0x7f).any()
+        later = codes[16:].copy()
+        later[4, 7] = want[20, 7]
+        assert np.array_equal(later, want[16:])
