@@ -490,6 +490,12 @@ typedef struct {
  * sees nothing, and one with pos < 0 (padding), gets out = 0 and lse = -inf.  All pointers are
  * DEVICE: slopes [Hq] fp32, first [B][T] and prefix [B] int32, each may be NULL.  A tq_scoring*
  * of NULL means scale = 1 / sqrt(d) and no option.
+ * Numbers: scores, their sums and outputs are fp32 (a capped score to 2^-19 of itself).  For 16-bit
+ * queries each probability, times the power of two of its value block, is rounded to 11 bits (fp32
+ * queries: 22).  That power counts from the largest value scale that the call has met so far in
+ * the query's group (the queries of a key head, up to 256 in a block of queries, 16 in a step): tokens
+ * whose value scale is more than 2^21 (a step: 2^29) below it lose bits, from 2^32 (2^40) on they
+ * count as 0.
  */
 typedef struct {
   float scale;
@@ -509,6 +515,7 @@ typedef struct {
  *   s = the smallest power of two >= 2^-126 with amax <= 448 s; where the block holds earlier
  *   tokens, s = max(s, its scale) and their codes become e4m3(code * old scale / s);
  *   code = e4m3(x / s), to nearest, ties to even.
+ * An infinity counts as 1.75 * 2^128 and takes the largest code, a NaN the NaN code and no part in s.
  * Records behind the last token keep their bytes.  A sequence whose lengths do not fit (new
  * tokens more than T or than kv_lens, kv_lens over capacity) is left alone and sets the device
  * status to TQ_ERR_INVALID_ARG.  Two sequences must not share a page that gets tokens.
@@ -557,8 +564,9 @@ tq_status tq_kv8_prefill_attn(const void* q, const tq_strides* q_strides, int32_
  * each row (sequence) holds, and how many rows hold each page.  block_table [rows][max_pages]
  * and refs [num_pages] are DEVICE int32 owned by the caller; refs 0 = free, start them at 0.
  * A row of len tokens holds its first ceil(len / page_size) entries; entries behind them are
- * not read.  Free pages are taken lowest id first, in the order of the requests, so that a
- * call's result depends on its arguments alone.
+ * not read, but for tq_pages_compact, which goes through the whole table: start it at -1.  Free
+ * pages are taken lowest id first, in the order of the requests, so that a call's result depends
+ * on its arguments alone.
  * A pool array is one array of the cache's records ([num_pages][page_bytes]: for the 8-bit
  * cache page_bytes = Hkv * page_size * d of codes, Hkv * page_size / TQ_KV8_BLOCK * 4 of
  * scales); page_bytes is a multiple of 4.

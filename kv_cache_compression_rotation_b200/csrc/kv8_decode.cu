@@ -4,7 +4,7 @@
 //   l_t = scale q.k^_t (capped, biased),  out = sum_t softmax(l)_t v^_t,  lse = ln sum_t e^{l_t}
 //
 // Bytes bound it: each token of a key head is 2 d codes and 2 / 16 scales, read once for all its
-// query rows (d = 128, eight sequences of 131072 tokens: 325 us, 6.6 TB/s).  Tiles of 8 KB of codes
+// query rows (d = 128, eight sequences of 131072 tokens: 322 us, 6.7 TB/s).  Tiles of 8 KB of codes
 // (32 tokens at d = 128, 64 at d = 64) of all (sequence, key head) pairs form one line that is cut
 // into equal parts, so ragged lengths and few long sequences load every SM alike: a part for each
 // CTA, whose warps take its tiles in turn, or one for each warp (the rule stands in plan_attn).  A
