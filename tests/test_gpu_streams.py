@@ -130,3 +130,22 @@ def test_quantized_records_are_not_zeroed_behind_the_call():
     got = K.quantize(q, x, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(got.codes, want.codes) and torch.equal(got.norms, want.norms)
+
+
+def test_captured_with_its_stream_named():
+    """A call that is captured on the stream it is given, with memory of its own, replays its bits."""
+    n, T = 4096, 100
+    kc, vc = cache8(n)
+    q, lens = ti.normal_torch((1, 8, T, D), 51, "cuda", torch.bfloat16), i32(n)
+    pos = torch.arange(n - T, n, dtype=torch.int32, device="cuda")[None]
+    run = lambda s=None: K.kv8_prefill_attn(q, pos, lens, kc, vc, 2, Nmax=n, return_lse=True, stream=s)
+    want, graph, stream = run(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        got = run(stream)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert K.get_status() == 0
