@@ -152,7 +152,6 @@ __device__ void scan_requests(const PagesParams& p) {
 enum : int { COUNT_FORK = 0, COUNT_RESERVE = 1, COUNT_COMPACT = 2 };
 
 // Blocks: the chunks, one for the requests, and for a fork those that look through the source rows.
-
 template <int MODE>
 __global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p) {
   __shared__ int sh[kThreads / 32];
